@@ -460,6 +460,154 @@ sdm_status sdm_weight_stats(int64_t rows, int32_t K, const float* w, float* cum,
                             void* ws, size_t ws_bytes, sdm_stream_t stream);
 
 /*
+ * ---- the state-space block beside an SDM layer ------------------------------------------------
+ * A hybrid stack mixes SDM layers with other linear recurrences (the pages' §4 compares with
+ * Gated DeltaNet, whose q, k and v pass through short convolutions, and with a state-space
+ * model).  These calls are that block's operators: the short causal convolution, the
+ * selective scan (for prompts and for single tokens) and the norms around a block, each with its
+ * gradient.  Conventions as above, except that activations are passed as views: last dimension
+ * contiguous, the other strides free, so that a column slice of a projection is passed without a
+ * copy.  A view's data needs only its element's alignment; every other pointer is 16-byte aligned
+ * unless a comment says otherwise.  An input stride may be 0 (a broadcast input); negative strides
+ * are refused, and an output's rows may not overlap each other (strides of at least a row where
+ * the extent is above 1) nor any input.
+ *
+ * Padded batches: lens [B] int32 (device, or NULL: every sequence has T tokens; 4-byte aligned)
+ * are the tokens of each sequence, taken as clamped to [0, T].  Tokens behind them are not read,
+ * move no state and leave their output rows as they were; their gradients are written as zero.
+ *
+ * Sums, states and softmax-free statistics are fp32; each output is rounded once to its type.
+ * Every result is the same from run to run (no atomics: sums over blocks are added in order).
+ */
+typedef struct {
+    void* data;          /* element (b, h, t, c) at data + b*sb + h*sh + t*st + c */
+    int64_t sb, sh, st;  /* strides in elements: sequence, head (or group), token */
+} sdm_view;
+
+/*
+ * Short causal convolution over the tokens, one filter of K taps per channel:
+ *   p_t = bias + sum_{j<K} w[j] x_{t-K+1+j},   y_t = p_t  or  p_t sigmoid(p_t)  (act)
+ * Tokens before the call come from the state: the last K-1 inputs of the sequence, oldest first.
+ * T = 1 is the form for single tokens (one call per decode step, the state moved on in place).
+ *   x, y   views [B][H][T][d] of x_dtype ([B][T][D] is H = 1)
+ *   w      [H][d][K] fp32;  bias [H][d] fp32 or NULL
+ *   state  [B][H][K-1][d] x_dtype, updated in place: read at the start unless dims->fresh is
+ *          set (then the start is zero), written at the end.  NULL: start at zero, keep nothing.
+ *          Ignored for K = 1.
+ * 1 <= K <= 8; B, H, d >= 1; T >= 0; B*H <= 65535.  One launch.
+ */
+typedef enum { SDM_ACT_NONE = 0, SDM_ACT_SILU = 1 } sdm_act;
+typedef struct {
+    int32_t B, H, T, d, K;
+    int32_t x_dtype; /* sdm_dtype of x, y and the state */
+    int32_t act;     /* sdm_act */
+    int32_t fresh;   /* 1: the sequences start here (the state's contents are not read) */
+} sdm_conv_dims;
+sdm_status sdm_short_conv(const sdm_conv_dims* dims, const sdm_view* x, const float* w,
+                          const float* bias, void* state, const int32_t* lens, const sdm_view* y,
+                          sdm_stream_t stream);
+
+/*
+ * Its gradient, for dy a view like y (x_dtype); p is computed again from x.
+ *   state      the state at the START of the call (read only), or NULL / fresh: zero
+ *   dstate_end [B][H][K-1][d] fp32: gradient with respect to the state after the call, or NULL
+ *   dx         view [B][H][T][d] x_dtype, written (zero behind lens)
+ *   dw [H][d][K], dbias [H][d] fp32, written (dbias may be NULL)
+ *   dstate     [B][H][K-1][d] fp32: gradient with respect to the start state, written, or NULL
+ *   ws         at least sdm_short_conv_backward_workspace_bytes(dims) bytes
+ * Two launches.
+ */
+size_t sdm_short_conv_backward_workspace_bytes(const sdm_conv_dims* dims);
+sdm_status sdm_short_conv_backward(const sdm_conv_dims* dims, const sdm_view* x, const float* w,
+                                   const float* bias, const void* state, const int32_t* lens,
+                                   const sdm_view* dy, const float* dstate_end,
+                                   const sdm_view* dx, float* dw, float* dbias, float* dstate,
+                                   void* ws, size_t ws_bytes, sdm_stream_t stream);
+
+/*
+ * Selective state-space scan: D channels of N states, B and C shared by the D/G channels of a
+ * group (channel c belongs to group c / (D/G)).  Per token t, channel c, state n:
+ *   s_t = softplus(delta_t + dt_bias)   (without the softplus if dims->softplus is 0)
+ *   h_t[n] = exp(s_t A[n]) h_{t-1}[n] + s_t B_t[n] u_t
+ *   y_t    = (sum_n C_t[n] h_t[n] + Dskip u_t) * z_t sigmoid(z_t)   (the last factor if z)
+ *   u, delta, z, y  views [B][T][D] of x_dtype (sh unused); z NULL: no gate
+ *   A [D][N] fp32; Dskip, dt_bias [D] fp32 or NULL
+ *   Bm, Cm  views [B][T][G][N] of x_dtype, sh the group's stride
+ *   state   [B][D][N] fp32, updated in place: read at the start unless dims->fresh is set (then
+ *           the start is zero), written at the end.  NULL: start at zero, keep nothing.
+ *   ws      at least sdm_selective_scan_workspace_bytes(dims) bytes (may be NULL when that is 0)
+ * 1 <= N <= 64; G divides D; B*G <= 65535.  T = 1 is the form for single tokens.  Long calls of
+ * few channels are split over time: one launch, or three.
+ */
+typedef struct {
+    int32_t B, T, D, N, G;
+    int32_t x_dtype;  /* sdm_dtype of u, delta, z, Bm, Cm, y */
+    int32_t softplus; /* 1: s = softplus(delta + dt_bias), 0: s = delta + dt_bias */
+    int32_t fresh;    /* 1: the sequences start here (the state's contents are not read) */
+} sdm_scan_dims;
+size_t sdm_selective_scan_workspace_bytes(const sdm_scan_dims* dims);
+sdm_status sdm_selective_scan(const sdm_scan_dims* dims, const sdm_view* u, const sdm_view* delta,
+                              const float* A, const sdm_view* Bm, const sdm_view* Cm,
+                              const float* Dskip, const sdm_view* z, const float* dt_bias,
+                              float* state, const int32_t* lens, const sdm_view* y, void* ws,
+                              size_t ws_bytes, sdm_stream_t stream);
+
+/*
+ * Its gradient, for dy a view like y; the states are computed again from the inputs.
+ *   state, dstate_end  [B][D][N] fp32: the state at the START of the call (NULL or fresh: zero)
+ *                      and the gradient with respect to the state after it (NULL: zero)
+ *   du, ddelta, dz     views [B][T][D] of x_dtype, written (dz NULL exactly when z is NULL)
+ *   dB, dC             [B][T][G][N] x_dtype, written
+ *   dA [D][N]; dDskip, ddt_bias [D] (each may be NULL); dstate [B][D][N] or NULL: fp32, written
+ *   ws                 at least sdm_selective_scan_backward_workspace_bytes(dims) bytes
+ * Up to five launches.
+ */
+size_t sdm_selective_scan_backward_workspace_bytes(const sdm_scan_dims* dims);
+sdm_status sdm_selective_scan_backward(
+    const sdm_scan_dims* dims, const sdm_view* u, const sdm_view* delta, const float* A,
+    const sdm_view* Bm, const sdm_view* Cm, const float* Dskip, const sdm_view* z,
+    const float* dt_bias, const float* state, const int32_t* lens, const sdm_view* dy,
+    const float* dstate_end, const sdm_view* du, const sdm_view* ddelta, float* dA, void* dB,
+    void* dC, float* dDskip, const sdm_view* dz, float* ddt_bias, float* dstate, void* ws,
+    size_t ws_bytes, sdm_stream_t stream);
+
+/*
+ * The norms around a block, with its gate and residual scale, over rows of D values: the block's
+ * output f is RMS-normalised, gated and scaled, added to the residual stream r, and the sum is
+ * RMS-normalised again as the next block's input:
+ *   p = f / sqrt(mean f^2 + eps) * w_post       (w_post NULL: p = f)
+ *   o = r + scale * sigmoid(gate) * p           (scale, gate NULL: 1)
+ *   r_out = o,   n = o / sqrt(mean o^2 + eps) * w_pre   (n from o before its rounding)
+ *   r, r_out [rows][D] r_dtype (r_out may be r, or NULL); f [rows][D] f_dtype
+ *   gate, n  [rows][D] x_dtype (n NULL: r_out only); w_post, scale, w_pre [D] fp32
+ * w_pre NULL: n without the weight.  1 <= D <= 16384; eps >= 0.  Rows contiguous.  One launch.
+ */
+typedef struct {
+    int64_t rows;
+    int32_t D;
+    int32_t r_dtype, f_dtype, x_dtype; /* sdm_dtype of r and r_out, of f, of gate and n */
+    float eps;
+} sdm_norm_dims;
+sdm_status sdm_block_norm(const sdm_norm_dims* dims, const void* r, const void* f,
+                          const float* w_post, const void* gate, const float* scale,
+                          const float* w_pre, void* r_out, void* n, sdm_stream_t stream);
+
+/*
+ * Its gradient; o is computed again from r and f.
+ *   dr_out [rows][D] r_dtype or NULL (zero), dn [rows][D] x_dtype or NULL (zero)
+ *   dr r_dtype, df f_dtype, dgate x_dtype [rows][D], dscale, dw_post, dw_pre [D] fp32: written.
+ *   dr, df and each gradient of an input that was NULL may be NULL (the last three sums always).
+ *   ws     at least sdm_block_norm_backward_workspace_bytes(dims) bytes
+ * Two launches.
+ */
+size_t sdm_block_norm_backward_workspace_bytes(const sdm_norm_dims* dims);
+sdm_status sdm_block_norm_backward(const sdm_norm_dims* dims, const void* r, const void* f,
+                                   const float* w_post, const void* gate, const float* scale,
+                                   const float* w_pre, const void* dr_out, const void* dn,
+                                   void* dr, void* df, void* dgate, float* dscale, float* dw_post,
+                                   float* dw_pre, void* ws, size_t ws_bytes, sdm_stream_t stream);
+
+/*
  * Read the device error word into *bits (host pointer; SDM_DEVERR_* bits), then
  * clear it when `clear` is non-zero.  Synchronises `stream`.  Returns SDM_OK when
  * no bit is set, SDM_ERR_BAD_INDEX when any is, SDM_ERR_CUDA if the copy fails.

@@ -776,7 +776,7 @@ const char* sdm_status_str(int32_t status) {
     }
 }
 
-int32_t sdm_abi_version(void) { return 4; }
+int32_t sdm_abi_version(void) { return 5; }
 
 sdm_status sdm_state_bytes(const sdm_dims* dims, size_t* M_bytes, size_t* stamp_bytes,
                            size_t* lambda_bytes) {

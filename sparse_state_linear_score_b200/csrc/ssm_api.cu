@@ -1,0 +1,625 @@
+// C ABI of the state-space block's operators (declared in include/sdm.h): host-side validation,
+// workspace layout and launches of the short convolution, the selective scan and the block norms.
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "../../include/sdm.h"
+#include "block_norm.cuh"
+#include "selective_scan.cuh"
+#include "selective_scan_bwd.cuh"
+#include "short_conv.cuh"
+
+using namespace sdm::ssm;
+
+namespace {
+
+constexpr int kSms = 148;
+constexpr int kMaxGrid = 65535;  // of a grid's second and third axis
+constexpr int kScanMaxT = 1 << 21;
+
+size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
+long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
+
+bool aligned(const void* p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
+
+size_t elem_bytes(int32_t dtype) { return dtype == SDM_BF16 ? 2 : 4; }
+
+bool known(int32_t dtype) { return dtype == SDM_F32 || dtype == SDM_BF16; }
+
+sdm_status launched() { return cudaGetLastError() == cudaSuccess ? SDM_OK : SDM_ERR_CUDA; }
+
+// A required input view; without tokens its data is not looked at.
+sdm_status check_in(const sdm_view* v, int32_t dtype, int64_t T) {
+    if (!v || (!v->data && T > 0)) return SDM_ERR_ARG;
+    if (v->sb < 0 || v->sh < 0 || v->st < 0) return SDM_ERR_ARG;
+    return aligned(v->data, elem_bytes(dtype)) ? SDM_OK : SDM_ERR_ALIGN;
+}
+
+// An output view of rows of `row` elements: its rows may not overlap.  The axes of more than one
+// entry, from the smallest stride up, have to nest: each stride clears what lies inside it.
+sdm_status check_out(const sdm_view* v, int32_t dtype, int64_t nb, int64_t nh, int64_t nt,
+                     int64_t row) {
+    const sdm_status e = check_in(v, dtype, nt);
+    if (e) return e;
+    struct Axis {
+        int64_t stride, n;
+    } ax[3] = {{v->sb, nb}, {v->sh, nh}, {v->st, nt}};
+    std::sort(ax, ax + 3, [](const Axis& a, const Axis& b) { return a.stride < b.stride; });
+    __int128 span = row;
+    for (const Axis& x : ax) {
+        if (x.n <= 1) continue;
+        if (x.stride < span) return SDM_ERR_ARG;
+        span += (__int128)x.stride * (x.n - 1);
+    }
+    return SDM_OK;
+}
+
+bool same_data(const sdm_view* a, const sdm_view* b, int64_t T) {
+    return a && T > 0 && a->data == b->data;
+}
+
+template <typename T>
+View<T> view(const sdm_view* v) {
+    if (!v) return View<T>{nullptr, 0, 0, 0};
+    return View<T>{static_cast<T*>(v->data), v->sb, v->sh, v->st};
+}
+
+// Four elements at a time where the rows allow it.
+bool vec4_ok(const sdm_view* v, int32_t dtype) {
+    return !v || (aligned(v->data, 4 * elem_bytes(dtype)) && v->sb % 4 == 0 && v->sh % 4 == 0 &&
+                  v->st % 4 == 0);
+}
+
+template <typename K>
+bool allow_smem(K kernel, size_t bytes) {
+    if (bytes <= 48 * 1024) return true;
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) ==
+           cudaSuccess;
+}
+
+// ---- short convolution ---------------------------------------------------------------------
+sdm_status check_conv(const sdm_conv_dims* d) {
+    if (!d) return SDM_ERR_ARG;
+    if (!known(d->x_dtype)) return SDM_ERR_DTYPE;
+    if (d->act != SDM_ACT_NONE && d->act != SDM_ACT_SILU) return SDM_ERR_ARG;
+    if (d->fresh != 0 && d->fresh != 1) return SDM_ERR_ARG;
+    if (d->B < 1 || d->H < 1 || d->d < 1 || d->T < 0 || d->T > (1 << 30)) return SDM_ERR_SHAPE;
+    if ((long long)d->B * d->H > kMaxGrid) return SDM_ERR_SHAPE;
+    if (d->K < 1 || d->K > CONV_MAXK) return SDM_ERR_SHAPE;
+    return SDM_OK;
+}
+
+struct ConvPlan {
+    int run, runs;
+    unsigned gx, gy;
+};
+
+// Tokens of a run: as long as there are enough warps (24 an SM hide the loads' latency), since a
+// run reads K-1 tokens of its neighbour.
+ConvPlan conv_plan(const sdm_conv_dims* d, int V) {
+    ConvPlan p;
+    p.gx = (unsigned)ceil_div((long long)d->H * (d->d / V), 32);
+    p.run = CONV_RUN_MIN;
+    while (p.run < 256 && (long long)p.gx * d->B * ceil_div(d->T, 2 * p.run) >= kSms * 24) p.run *= 2;
+    while (ceil_div((long long)d->B * ceil_div(d->T, p.run), CONV_WARPS) > kMaxGrid) p.run *= 2;
+    p.runs = (int)std::max(1LL, ceil_div(d->T, p.run));
+    p.gy = (unsigned)ceil_div((long long)d->B * p.runs, CONV_WARPS);
+    return p;
+}
+
+// The gradient's blocks along the runs: their shares of dw are added afterwards.
+constexpr int kConvBwdRun = 64;
+constexpr int kConvBwdBlocks = 64;
+ConvPlan conv_bwd_plan(const sdm_conv_dims* d, int V) {
+    ConvPlan p;
+    p.gx = (unsigned)ceil_div((long long)d->H * (d->d / V), 32);
+    p.run = kConvBwdRun;
+    p.runs = (int)std::max(1LL, ceil_div(d->T, p.run));
+    const long long warps = (long long)d->B * p.runs;
+    p.gy = (unsigned)std::min<long long>(kConvBwdBlocks, ceil_div(warps, CONV_WARPS));
+    return p;
+}
+
+template <typename T, int V, int K>
+void launch_conv(const ConvArgs<T>& a, const ConvPlan& p, bool bwd, cudaStream_t s) {
+    const dim3 grid(p.gx, p.gy);
+    if (bwd) short_conv_bwd_kernel<T, V, K><<<grid, CONV_WARPS * 32, 0, s>>>(a);
+    else short_conv_kernel<T, V, K><<<grid, CONV_WARPS * 32, 0, s>>>(a);
+}
+
+template <typename T, int V>
+void launch_conv_k(const ConvArgs<T>& a, const ConvPlan& p, bool bwd, cudaStream_t s) {
+    switch (a.K) {
+        case 1: return launch_conv<T, V, 1>(a, p, bwd, s);
+        case 2: return launch_conv<T, V, 2>(a, p, bwd, s);
+        case 3: return launch_conv<T, V, 3>(a, p, bwd, s);
+        case 4: return launch_conv<T, V, 4>(a, p, bwd, s);
+        case 5: return launch_conv<T, V, 5>(a, p, bwd, s);
+        case 6: return launch_conv<T, V, 6>(a, p, bwd, s);
+        case 7: return launch_conv<T, V, 7>(a, p, bwd, s);
+        default: return launch_conv<T, V, 8>(a, p, bwd, s);
+    }
+}
+
+template <typename T>
+ConvArgs<T> conv_args(const sdm_conv_dims* d, const sdm_view* x, const float* w, const float* bias,
+                      const void* state, const int32_t* lens) {
+    ConvArgs<T> a{};
+    a.x = view<const T>(x);
+    a.w = w;
+    a.bias = bias;
+    a.state = d->K > 1 ? static_cast<T*>(const_cast<void*>(state)) : nullptr;
+    a.lens = lens;
+    a.B = d->B, a.H = d->H, a.T_ = d->T, a.d = d->d, a.K = d->K, a.act = d->act, a.fresh = d->fresh;
+    return a;
+}
+
+template <typename T>
+sdm_status run_conv(const sdm_conv_dims* d, const sdm_view* x, const float* w, const float* bias,
+                    void* state, const int32_t* lens, const sdm_view* y, cudaStream_t s) {
+    ConvArgs<T> a = conv_args<T>(d, x, w, bias, state, lens);
+    a.y = view<T>(y);
+    const bool v4 = d->d % 4 == 0 && vec4_ok(x, d->x_dtype) && vec4_ok(y, d->x_dtype);
+    const ConvPlan p = conv_plan(d, v4 ? 4 : 1);
+    a.run = p.run, a.runs = p.runs;
+    if (v4) launch_conv_k<T, 4>(a, p, false, s);
+    else launch_conv_k<T, 1>(a, p, false, s);
+    return launched();
+}
+
+template <typename T>
+sdm_status run_conv_bwd(const sdm_conv_dims* d, const sdm_view* x, const float* w,
+                        const float* bias, const void* state, const int32_t* lens,
+                        const sdm_view* dy, const float* dstate_end, const sdm_view* dx, float* dw,
+                        float* dbias, float* dstate, void* ws, cudaStream_t s) {
+    ConvArgs<T> a = conv_args<T>(d, x, w, bias, state, lens);
+    a.y = view<T>(dx);
+    a.dy = view<const T>(dy);
+    a.dstate_end = d->K > 1 ? dstate_end : nullptr;
+    a.dstate = d->K > 1 ? dstate : nullptr;
+    a.part = static_cast<float*>(ws);
+    const bool v4 = d->d % 4 == 0 && vec4_ok(x, d->x_dtype) && vec4_ok(dy, d->x_dtype) &&
+                    vec4_ok(dx, d->x_dtype);
+    const ConvPlan p = conv_bwd_plan(d, v4 ? 4 : 1);
+    a.run = p.run, a.runs = p.runs;
+    if (v4) launch_conv_k<T, 4>(a, p, true, s);
+    else launch_conv_k<T, 1>(a, p, true, s);
+    const sdm_status e = launched();
+    if (e) return e;
+    const long long C = (long long)d->H * d->d;
+    conv_sum_kernel<<<(unsigned)ceil_div(C * (d->K + 1), 256), 256, 0, s>>>(a.part, (int)p.gy, C,
+                                                                           d->K, dw, dbias);
+    return launched();
+}
+
+// ---- selective scan ------------------------------------------------------------------------
+sdm_status check_scan(const sdm_scan_dims* d) {
+    if (!d) return SDM_ERR_ARG;
+    if (!known(d->x_dtype)) return SDM_ERR_DTYPE;
+    if (d->softplus != 0 && d->softplus != 1) return SDM_ERR_ARG;
+    if (d->fresh != 0 && d->fresh != 1) return SDM_ERR_ARG;
+    if (d->B < 1 || d->D < 1 || d->G < 1 || d->T < 0 || d->T > kScanMaxT) return SDM_ERR_SHAPE;
+    if (d->N < 1 || d->N > 64 || d->D % d->G != 0) return SDM_ERR_SHAPE;
+    if ((long long)d->B * d->G > kMaxGrid) return SDM_ERR_SHAPE;
+    return SDM_OK;
+}
+
+int pad_states(int N) { return N <= 8 ? 8 : (N <= 16 ? 16 : (N <= 32 ? 32 : 64)); }
+
+struct ScanPlan {
+    int NN, LN;         // states with padding, lanes of a channel
+    int chunk, nchunk;  // tokens of a chunk
+    unsigned gx;
+    size_t off_S, total;
+};
+
+long long scan_warps(const sdm_scan_dims* d, int LN) {
+    return (long long)d->B * d->G * ceil_div(d->D / d->G, SCAN_THREADS / LN) * (SCAN_THREADS / 32);
+}
+
+// Lanes of a channel: as few as give every SM sub-partition a warp (fewer lanes share less work,
+// more lanes make more warps); then chunks of the tokens while half of the sub-partitions would
+// idle, since a second pass over the exponentials costs about as much as it gains above that.
+ScanPlan scan_plan(const sdm_scan_dims* d) {
+    ScanPlan p{};
+    p.NN = pad_states(d->N);
+    const int lo = p.NN <= 16 ? 1 : p.NN / 16, hi = p.NN == 8 ? 2 : (p.NN == 16 ? 4 : p.NN / 8);
+    p.LN = lo;
+    while (p.LN < hi && scan_warps(d, p.LN) < 4 * kSms) p.LN *= 2;
+    const long long warps = scan_warps(d, p.LN);
+    p.chunk = std::max(1, d->T);
+    p.nchunk = 1;
+    if (warps <= 2 * kSms) {
+        const long long want = std::min(ceil_div(d->T, 64), 8 * kSms / warps);
+        if (want > 1) {
+            p.chunk = (int)(ceil_div(ceil_div(d->T, want), SCAN_TILE) * SCAN_TILE);
+            p.nchunk = (int)ceil_div(d->T, p.chunk);
+        }
+    }
+    p.gx = (unsigned)(d->G * ceil_div(d->D / d->G, SCAN_THREADS / p.LN));
+    const size_t bc = (size_t)d->B * p.nchunk * d->D;
+    if (p.nchunk > 1) {
+        p.off_S = up256(bc * d->N * 4);
+        p.total = up256(p.off_S + bc * 4);
+    }
+    return p;
+}
+
+template <typename T>
+ScanArgs<T> scan_args(const sdm_scan_dims* d, const sdm_view* u, const sdm_view* delta,
+                      const float* A, const sdm_view* Bm, const sdm_view* Cm, const float* Dskip,
+                      const sdm_view* z, const float* dt_bias, const float* state,
+                      const int32_t* lens) {
+    ScanArgs<T> a{};
+    a.u = view<const T>(u), a.delta = view<const T>(delta), a.z = view<const T>(z);
+    a.Bm = view<const T>(Bm), a.Cm = view<const T>(Cm);
+    a.A = A, a.Dskip = Dskip, a.dt_bias = dt_bias;
+    a.state = const_cast<float*>(state);
+    a.lens = lens;
+    a.B = d->B, a.T_ = d->T, a.D = d->D, a.N = d->N, a.G = d->G;
+    a.softplus = d->softplus, a.fresh = d->fresh;
+    return a;
+}
+
+template <typename T, int NPT, int LN>
+void launch_scan_t(const ScanArgs<T>& a, const ScanPlan& p, cudaStream_t s) {
+    if (p.nchunk > 1) {
+        scan_chunk_kernel<T, NPT, LN, false>
+            <<<dim3(p.gx, p.nchunk - 1, a.B), SCAN_THREADS, 0, s>>>(a);
+        const long long n = (long long)a.B * a.D * a.N;
+        scan_carry_kernel<T><<<(unsigned)ceil_div(n, 256), 256, 0, s>>>(a, 0);
+    }
+    scan_out_kernel<T, NPT, LN><<<dim3(p.gx, p.nchunk, a.B), SCAN_THREADS, 0, s>>>(a);
+}
+
+template <typename T>
+void launch_step(const ScanArgs<T>& a, int NN, cudaStream_t s) {
+    const int LN = NN / 4;
+    const dim3 grid((unsigned)ceil_div(a.D, 256 / LN), a.B);
+    if (NN == 8) scan_step_kernel<T, 2><<<grid, 256, 0, s>>>(a);
+    else if (NN == 16) scan_step_kernel<T, 4><<<grid, 256, 0, s>>>(a);
+    else if (NN == 32) scan_step_kernel<T, 8><<<grid, 256, 0, s>>>(a);
+    else scan_step_kernel<T, 16><<<grid, 256, 0, s>>>(a);
+}
+
+template <typename T>
+sdm_status run_scan(const sdm_scan_dims* d, ScanArgs<T> a, const sdm_view* y, void* ws,
+                    cudaStream_t s) {
+    a.y = view<T>(y);
+    if (d->T == 1) {
+        launch_step<T>(a, pad_states(d->N), s);
+        return launched();
+    }
+    const ScanPlan p = scan_plan(d);
+    a.chunk = p.chunk, a.nchunk = p.nchunk;
+    a.E = static_cast<float*>(ws);
+    a.S = reinterpret_cast<float*>(static_cast<char*>(ws) + p.off_S);
+    if (p.NN == 8) {
+        if (p.LN == 1) launch_scan_t<T, 8, 1>(a, p, s);
+        else launch_scan_t<T, 4, 2>(a, p, s);
+    } else if (p.NN == 16) {
+        if (p.LN == 1) launch_scan_t<T, 16, 1>(a, p, s);
+        else if (p.LN == 2) launch_scan_t<T, 8, 2>(a, p, s);
+        else launch_scan_t<T, 4, 4>(a, p, s);
+    } else if (p.NN == 32) {
+        if (p.LN == 2) launch_scan_t<T, 16, 2>(a, p, s);
+        else launch_scan_t<T, 8, 4>(a, p, s);
+    } else {
+        if (p.LN == 4) launch_scan_t<T, 16, 4>(a, p, s);
+        else launch_scan_t<T, 8, 8>(a, p, s);
+    }
+    return launched();
+}
+
+struct ScanBwdPlan {
+    int NN, nchunk, tiles, blocks;
+    size_t off_R, off_S, off_a, off_d, off_bc, total;
+};
+
+ScanBwdPlan scan_bwd_plan(const sdm_scan_dims* d) {
+    ScanBwdPlan p{};
+    p.NN = pad_states(d->N);
+    p.nchunk = (int)std::max(1LL, ceil_div(d->T, BWD_CHUNK));
+    const int ch = BWD_THREADS / (p.NN / 4), all = (int)ceil_div(d->D / d->G, ch);
+    // channel tiles of a block: more tiles, fewer shares of dB and dC to write and add; as many
+    // as leave four blocks an SM
+    const long long rest = (long long)d->B * p.nchunk * d->G;
+    const long long want = std::max(1LL, std::min<long long>(all, ceil_div(4 * kSms, rest)));
+    p.tiles = (int)ceil_div(all, want);
+    p.blocks = (int)ceil_div(all, p.tiles);
+    const size_t bk = (size_t)d->B * p.nchunk, states = bk * d->D * d->N * 4;
+    size_t o = 0;
+    if (p.nchunk > 1) {
+        o = up256(o + states);
+        p.off_R = o, o = up256(o + states);
+        p.off_S = o, o = up256(o + bk * d->D * 4);
+    }
+    p.off_a = o, o = up256(o + states);
+    p.off_d = o, o = up256(o + bk * d->D * 8);
+    p.off_bc = o, o = up256(o + (size_t)p.blocks * d->B * d->T * d->G * 2 * d->N * 4);
+    p.total = o;
+    return p;
+}
+
+template <typename T, int LN>
+sdm_status launch_scan_bwd_t(const ScanBwdArgs<T>& A, const ScanBwdPlan& p, cudaStream_t s) {
+    const ScanArgs<T>& a = A.s;
+    constexpr int NN = LN * BWD_NPT, CLN = NN / 8;
+    if (p.nchunk > 1) {
+        const unsigned gx = (unsigned)(a.G * ceil_div(a.D / a.G, SCAN_THREADS / CLN));
+        scan_chunk_kernel<T, 8, CLN, true><<<dim3(gx, p.nchunk, a.B), SCAN_THREADS, 0, s>>>(a);
+        const unsigned n = (unsigned)ceil_div((long long)a.B * a.D * a.N, 256);
+        scan_carry_kernel<T><<<n, 256, 0, s>>>(a, 0);
+        scan_carry_kernel<T><<<n, 256, 0, s>>>(a, 1);
+    }
+    const size_t smem = bwd_smem(NN);
+    if (!allow_smem(scan_bwd_kernel<T, LN>, smem)) return SDM_ERR_CUDA;
+    scan_bwd_kernel<T, LN>
+        <<<dim3((unsigned)(a.G * p.blocks), p.nchunk, a.B), BWD_THREADS, smem, s>>>(A);
+    return launched();
+}
+
+template <typename T>
+sdm_status run_scan_bwd(const sdm_scan_dims* d, ScanArgs<T> a, const sdm_view* dy,
+                        const float* dstate_end, const sdm_view* du, const sdm_view* ddelta,
+                        float* dA, void* dB, void* dC, float* dDskip, const sdm_view* dz,
+                        float* ddt_bias, float* dstate, void* ws, cudaStream_t s) {
+    const ScanBwdPlan p = scan_bwd_plan(d);
+    char* base = static_cast<char*>(ws);
+    a.dy = view<const T>(dy);
+    a.dstate_end = dstate_end;
+    a.chunk = BWD_CHUNK, a.nchunk = p.nchunk;
+    a.E = reinterpret_cast<float*>(base);
+    a.R = reinterpret_cast<float*>(base + p.off_R);
+    a.S = reinterpret_cast<float*>(base + p.off_S);
+    ScanBwdArgs<T> A{};
+    A.s = a;
+    A.du = view<T>(du), A.ddelta = view<T>(ddelta), A.dz = view<T>(dz);
+    A.part_a = reinterpret_cast<float*>(base + p.off_a);
+    A.part_d = reinterpret_cast<float*>(base + p.off_d);
+    A.part_bc = reinterpret_cast<float*>(base + p.off_bc);
+    A.dstate = dstate;
+    A.tiles = p.tiles, A.blocks = p.blocks;
+    sdm_status e;
+    if (p.NN == 8) e = launch_scan_bwd_t<T, 2>(A, p, s);
+    else if (p.NN == 16) e = launch_scan_bwd_t<T, 4>(A, p, s);
+    else if (p.NN == 32) e = launch_scan_bwd_t<T, 8>(A, p, s);
+    else e = launch_scan_bwd_t<T, 16>(A, p, s);
+    if (e) return e;
+    const long long btg = (long long)d->B * d->T * d->G;
+    if (btg > 0)
+        scan_bc_sum_kernel<T><<<(unsigned)ceil_div(btg * 2 * d->N, 256), 256, 0, s>>>(
+            A.part_bc, p.blocks, btg, d->N, static_cast<T*>(dB), static_cast<T*>(dC));
+    const long long na = (long long)d->D * d->N;
+    scan_param_sum_kernel<<<(unsigned)ceil_div(na + 2LL * d->D, 32), 32 * DSUM_SEG, 0, s>>>(
+        A.part_a, A.part_d, (long long)d->B * p.nchunk, na, d->D, dA, dDskip, ddt_bias);
+    return launched();
+}
+
+sdm_status check_scan_in(const sdm_scan_dims* d, const sdm_view* u, const sdm_view* delta,
+                         const float* A, const sdm_view* Bm, const sdm_view* Cm,
+                         const float* Dskip, const sdm_view* z, const float* dt_bias,
+                         const float* state, const int32_t* lens) {
+    sdm_status e = check_scan(d);
+    if (e) return e;
+    if ((e = check_in(u, d->x_dtype, d->T)) || (e = check_in(delta, d->x_dtype, d->T)) ||
+        (e = check_in(Bm, d->x_dtype, d->T)) || (e = check_in(Cm, d->x_dtype, d->T)))
+        return e;
+    if (z && (e = check_in(z, d->x_dtype, d->T))) return e;
+    if (!A) return SDM_ERR_ARG;
+    if (!aligned(A, 16) || !aligned(Dskip, 16) || !aligned(dt_bias, 16) || !aligned(state, 16) ||
+        !aligned(lens, 4))
+        return SDM_ERR_ALIGN;
+    return SDM_OK;
+}
+
+// ---- block norms ---------------------------------------------------------------------------
+constexpr int kNormThreads = 512;
+constexpr int kNormBwdBlocks = 2 * kSms;
+
+sdm_status check_norm(const sdm_norm_dims* d) {
+    if (!d) return SDM_ERR_ARG;
+    if (!known(d->r_dtype) || !known(d->f_dtype) || !known(d->x_dtype)) return SDM_ERR_DTYPE;
+    if (d->rows < 0 || d->D < 1 || d->D > 16384) return SDM_ERR_SHAPE;
+    if (!(d->eps >= 0.f)) return SDM_ERR_ARG;
+    return SDM_OK;
+}
+
+NormArgs norm_args(const sdm_norm_dims* d, const void* r, const void* f, const float* w_post,
+                   const void* gate, const float* scale, const float* w_pre) {
+    NormArgs a{};
+    a.r = r, a.f = f, a.gate = gate;
+    a.w_post = w_post, a.scale = scale, a.w_pre = w_pre;
+    a.rows = d->rows, a.D = d->D, a.eps = d->eps;
+    a.rb = d->r_dtype == SDM_BF16, a.fb = d->f_dtype == SDM_BF16, a.xb = d->x_dtype == SDM_BF16;
+    return a;
+}
+
+template <int V, int P>
+void launch_norm(const NormArgs& a, bool bwd, unsigned grid, cudaStream_t s) {
+    const long long nv = a.D / V;
+    const unsigned nt = (unsigned)(ceil_div(ceil_div(nv, P), 32) * 32);
+    if (bwd) block_norm_bwd_kernel<V, P><<<grid, nt, 0, s>>>(a);
+    else block_norm_kernel<V, P><<<grid, nt, 0, s>>>(a);
+}
+
+// Values of a thread: few, so that the weights and a row fit its registers, in at most 512
+// threads.
+void launch_norm_any(const NormArgs& a, bool bwd, unsigned grid, cudaStream_t s) {
+    if (a.D % 4 == 0) {
+        if (a.D <= 2 * 4 * kNormThreads) return launch_norm<4, 2>(a, bwd, grid, s);
+        if (a.D <= 4 * 4 * kNormThreads) return launch_norm<4, 4>(a, bwd, grid, s);
+        return launch_norm<4, 8>(a, bwd, grid, s);
+    }
+    if (a.D <= 8 * kNormThreads) return launch_norm<1, 8>(a, bwd, grid, s);
+    return launch_norm<1, 32>(a, bwd, grid, s);
+}
+
+}  // namespace
+
+extern "C" {
+
+sdm_status sdm_short_conv(const sdm_conv_dims* dims, const sdm_view* x, const float* w,
+                          const float* bias, void* state, const int32_t* lens, const sdm_view* y,
+                          sdm_stream_t stream) {
+    sdm_status e = check_conv(dims);
+    if (e) return e;
+    if ((e = check_in(x, dims->x_dtype, dims->T))) return e;
+    if ((e = check_out(y, dims->x_dtype, dims->B, dims->H, dims->T, dims->d))) return e;
+    if (!w || same_data(x, y, dims->T)) return SDM_ERR_ARG;
+    if (!aligned(w, 16) || !aligned(bias, 16) || !aligned(state, 16) || !aligned(lens, 4))
+        return SDM_ERR_ALIGN;
+    if (dims->x_dtype == SDM_BF16) return run_conv<bf16>(dims, x, w, bias, state, lens, y, stream);
+    return run_conv<float>(dims, x, w, bias, state, lens, y, stream);
+}
+
+size_t sdm_short_conv_backward_workspace_bytes(const sdm_conv_dims* dims) {
+    if (check_conv(dims) != SDM_OK) return 0;
+    const ConvPlan p = conv_bwd_plan(dims, 1);  // its second axis does not depend on the width
+    return up256((size_t)p.gy * (dims->K + 1) * dims->H * dims->d * 4);
+}
+
+sdm_status sdm_short_conv_backward(const sdm_conv_dims* dims, const sdm_view* x, const float* w,
+                                   const float* bias, const void* state, const int32_t* lens,
+                                   const sdm_view* dy, const float* dstate_end,
+                                   const sdm_view* dx, float* dw, float* dbias, float* dstate,
+                                   void* ws, size_t ws_bytes, sdm_stream_t stream) {
+    sdm_status e = check_conv(dims);
+    if (e) return e;
+    if ((e = check_in(x, dims->x_dtype, dims->T)) || (e = check_in(dy, dims->x_dtype, dims->T))) return e;
+    if ((e = check_out(dx, dims->x_dtype, dims->B, dims->H, dims->T, dims->d))) return e;
+    if (!w || !dw || same_data(x, dx, dims->T) || same_data(dy, dx, dims->T)) return SDM_ERR_ARG;
+    if (!aligned(w, 16) || !aligned(bias, 16) || !aligned(state, 16) || !aligned(lens, 4) ||
+        !aligned(dstate_end, 16) || !aligned(dw, 16) || !aligned(dbias, 16) || !aligned(dstate, 16))
+        return SDM_ERR_ALIGN;
+    if (!ws || ws_bytes < sdm_short_conv_backward_workspace_bytes(dims)) return SDM_ERR_WORKSPACE;
+    if (!aligned(ws, 16)) return SDM_ERR_ALIGN;
+    if (dims->x_dtype == SDM_BF16)
+        return run_conv_bwd<bf16>(dims, x, w, bias, state, lens, dy, dstate_end, dx, dw, dbias,
+                                  dstate, ws, stream);
+    return run_conv_bwd<float>(dims, x, w, bias, state, lens, dy, dstate_end, dx, dw, dbias, dstate,
+                               ws, stream);
+}
+
+size_t sdm_selective_scan_workspace_bytes(const sdm_scan_dims* dims) {
+    if (check_scan(dims) != SDM_OK || dims->T <= 1) return 0;
+    return scan_plan(dims).total;
+}
+
+sdm_status sdm_selective_scan(const sdm_scan_dims* dims, const sdm_view* u, const sdm_view* delta,
+                              const float* A, const sdm_view* Bm, const sdm_view* Cm,
+                              const float* Dskip, const sdm_view* z, const float* dt_bias,
+                              float* state, const int32_t* lens, const sdm_view* y, void* ws,
+                              size_t ws_bytes, sdm_stream_t stream) {
+    sdm_status e = check_scan_in(dims, u, delta, A, Bm, Cm, Dskip, z, dt_bias, state, lens);
+    if (e) return e;
+    if ((e = check_out(y, dims->x_dtype, dims->B, 1, dims->T, dims->D))) return e;
+    for (const sdm_view* in : {u, delta, z, Bm, Cm})
+        if (same_data(in, y, dims->T)) return SDM_ERR_ARG;
+    const size_t need = sdm_selective_scan_workspace_bytes(dims);
+    if (need && (!ws || ws_bytes < need)) return SDM_ERR_WORKSPACE;
+    if (!aligned(ws, 16)) return SDM_ERR_ALIGN;
+    if (dims->x_dtype == SDM_BF16)
+        return run_scan<bf16>(dims, scan_args<bf16>(dims, u, delta, A, Bm, Cm, Dskip, z, dt_bias,
+                                                    state, lens), y, ws, stream);
+    return run_scan<float>(dims, scan_args<float>(dims, u, delta, A, Bm, Cm, Dskip, z, dt_bias,
+                                                  state, lens), y, ws, stream);
+}
+
+size_t sdm_selective_scan_backward_workspace_bytes(const sdm_scan_dims* dims) {
+    if (check_scan(dims) != SDM_OK) return 0;
+    return scan_bwd_plan(dims).total;
+}
+
+sdm_status sdm_selective_scan_backward(
+    const sdm_scan_dims* dims, const sdm_view* u, const sdm_view* delta, const float* A,
+    const sdm_view* Bm, const sdm_view* Cm, const float* Dskip, const sdm_view* z,
+    const float* dt_bias, const float* state, const int32_t* lens, const sdm_view* dy,
+    const float* dstate_end, const sdm_view* du, const sdm_view* ddelta, float* dA, void* dB,
+    void* dC, float* dDskip, const sdm_view* dz, float* ddt_bias, float* dstate, void* ws,
+    size_t ws_bytes, sdm_stream_t stream) {
+    sdm_status e = check_scan_in(dims, u, delta, A, Bm, Cm, Dskip, z, dt_bias, state, lens);
+    if (e) return e;
+    if ((e = check_in(dy, dims->x_dtype, dims->T))) return e;
+    if ((z != nullptr) != (dz != nullptr) || !dA) return SDM_ERR_ARG;
+    if (dims->T > 0 && (!dB || !dC)) return SDM_ERR_ARG;
+    const sdm_view* outs[3] = {du, ddelta, dz};
+    for (int i = 0; i < 3; ++i) {
+        if (i == 2 && !dz) break;
+        if ((e = check_out(outs[i], dims->x_dtype, dims->B, 1, dims->T, dims->D))) return e;
+        for (const sdm_view* in : {u, delta, z, Bm, Cm, dy})
+            if (same_data(in, outs[i], dims->T)) return SDM_ERR_ARG;
+        for (int j = 0; j < i; ++j)
+            if (same_data(outs[j], outs[i], dims->T)) return SDM_ERR_ARG;
+    }
+    if (!aligned(dstate_end, 16) || !aligned(dA, 16) || !aligned(dB, 16) || !aligned(dC, 16) ||
+        !aligned(dDskip, 16) || !aligned(ddt_bias, 16) || !aligned(dstate, 16))
+        return SDM_ERR_ALIGN;
+    if (!ws || ws_bytes < sdm_selective_scan_backward_workspace_bytes(dims))
+        return SDM_ERR_WORKSPACE;
+    if (!aligned(ws, 16)) return SDM_ERR_ALIGN;
+    if (dims->x_dtype == SDM_BF16)
+        return run_scan_bwd<bf16>(dims, scan_args<bf16>(dims, u, delta, A, Bm, Cm, Dskip, z,
+                                                        dt_bias, state, lens),
+                                  dy, dstate_end, du, ddelta, dA, dB, dC, dDskip, dz, ddt_bias,
+                                  dstate, ws, stream);
+    return run_scan_bwd<float>(dims, scan_args<float>(dims, u, delta, A, Bm, Cm, Dskip, z, dt_bias,
+                                                      state, lens),
+                               dy, dstate_end, du, ddelta, dA, dB, dC, dDskip, dz, ddt_bias, dstate,
+                               ws, stream);
+}
+
+sdm_status sdm_block_norm(const sdm_norm_dims* dims, const void* r, const void* f,
+                          const float* w_post, const void* gate, const float* scale,
+                          const float* w_pre, void* r_out, void* n, sdm_stream_t stream) {
+    sdm_status e = check_norm(dims);
+    if (e) return e;
+    if (dims->rows > 0 && (!r || !f || (!r_out && !n))) return SDM_ERR_ARG;
+    if (!aligned(r, 16) || !aligned(f, 16) || !aligned(w_post, 16) || !aligned(gate, 16) ||
+        !aligned(scale, 16) || !aligned(w_pre, 16) || !aligned(r_out, 16) || !aligned(n, 16))
+        return SDM_ERR_ALIGN;
+    if (dims->rows == 0) return SDM_OK;
+    NormArgs a = norm_args(dims, r, f, w_post, gate, scale, w_pre);
+    a.r_out = r_out, a.n = n;
+    const unsigned grid = (unsigned)std::min<long long>(dims->rows, kSms * 4);
+    launch_norm_any(a, false, grid, stream);
+    return launched();
+}
+
+size_t sdm_block_norm_backward_workspace_bytes(const sdm_norm_dims* dims) {
+    if (check_norm(dims) != SDM_OK) return 0;
+    const size_t blocks = (size_t)std::min<long long>(dims->rows, kNormBwdBlocks);
+    return up256(std::max<size_t>(1, blocks) * 3 * dims->D * 4);
+}
+
+sdm_status sdm_block_norm_backward(const sdm_norm_dims* dims, const void* r, const void* f,
+                                   const float* w_post, const void* gate, const float* scale,
+                                   const float* w_pre, const void* dr_out, const void* dn,
+                                   void* dr, void* df, void* dgate, float* dscale, float* dw_post,
+                                   float* dw_pre, void* ws, size_t ws_bytes, sdm_stream_t stream) {
+    sdm_status e = check_norm(dims);
+    if (e) return e;
+    if (dims->rows > 0 && (!r || !f)) return SDM_ERR_ARG;
+    if ((dgate && !gate) || (dw_post && !w_post)) return SDM_ERR_ARG;
+    const void* ptrs[] = {r, f, w_post, gate, scale, w_pre, dr_out, dn, dr, df, dgate, dscale,
+                          dw_post, dw_pre};
+    for (const void* p : ptrs)
+        if (!aligned(p, 16)) return SDM_ERR_ALIGN;
+    if (!ws || ws_bytes < sdm_block_norm_backward_workspace_bytes(dims)) return SDM_ERR_WORKSPACE;
+    if (!aligned(ws, 16)) return SDM_ERR_ALIGN;
+    NormArgs a = norm_args(dims, r, f, w_post, gate, scale, w_pre);
+    a.dr_out = dr_out, a.dn = dn;
+    a.dr = dr, a.df = df, a.dgate = dgate;
+    a.part = static_cast<float*>(ws);
+    const unsigned grid = (unsigned)std::min<long long>(dims->rows, kNormBwdBlocks);
+    if (grid > 0) {
+        launch_norm_any(a, true, grid, stream);
+        if ((e = launched())) return e;
+    }
+    norm_sum_kernel<<<(unsigned)ceil_div(3LL * dims->D, 32), 32 * SUM_SEG, 0, stream>>>(
+        a.part, (int)grid, dims->D, dscale, dw_post, dw_pre);
+    return launched();
+}
+
+}  // extern "C"
