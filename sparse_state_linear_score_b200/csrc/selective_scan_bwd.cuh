@@ -74,12 +74,12 @@ __global__ void __launch_bounds__(BWD_THREADS) scan_bwd_kernel(ScanBwdArgs<T> A)
     const long long pc = (long long)b * a.nchunk + ck;
 
     {  // the chunk's B and C, zero behind the sequence
-        const T* Bp = a.Bm.p + b * a.Bm.sb + g * a.Bm.sh;
-        const T* Cp = a.Cm.p + b * a.Cm.sb + g * a.Cm.sh;
+        const T* Bp = a.Bm.v.p + b * a.Bm.v.sb + g * a.Bm.v.sh;
+        const T* Cp = a.Cm.v.p + b * a.Cm.v.sb + g * a.Cm.v.sh;
         for (int e = tid; e < BWD_CHUNK * 2 * NN; e += BWD_THREADS) {
             const int t = t0 + e / (2 * NN), k = e % (2 * NN), n = k % NN;
             float v = 0.f;
-            if (t < t1 && n < a.N) v = k < NN ? ld(Bp + t * a.Bm.st + n) : ld(Cp + t * a.Cm.st + n);
+            if (t < t1 && n < a.N) v = k < NN ? ld(Bp + t * a.Bm.v.st + n) : ld(Cp + t * a.Cm.v.st + n);
             s_bc[e] = v;
             s_acc[e] = 0.f;
         }
@@ -91,10 +91,10 @@ __global__ void __launch_bounds__(BWD_THREADS) scan_bwd_kernel(ScanBwdArgs<T> A)
         if ((blk * A.tiles + tile) * CH >= dg) break;  // the same for the whole block
         const bool live = cg < dg;
         const int c = g * dg + (live ? cg : 0);
-        const T* up = a.u.p + b * a.u.sb + c;
-        const T* dp = a.delta.p + b * a.delta.sb + c;
-        const T* zp = a.z.p ? a.z.p + b * a.z.sb + c : nullptr;
-        const T* yp = a.dy.p + b * a.dy.sb + c;
+        const T* up = a.u.v.p + b * a.u.v.sb + c;
+        const T* dp = a.delta.v.p + b * a.delta.v.sb + c;
+        const T* zp = a.z.v.p ? a.z.v.p + b * a.z.v.sb + c : nullptr;
+        const T* yp = a.dy.v.p + b * a.dy.v.sb + c;
         const float bias = a.dt_bias ? a.dt_bias[c] : 0.f;
         const float skip = a.Dskip ? a.Dskip[c] : 0.f;
         float A2[NPT], h[NPT], gr[NPT], dA[NPT];
@@ -130,9 +130,9 @@ __global__ void __launch_bounds__(BWD_THREADS) scan_bwd_kernel(ScanBwdArgs<T> A)
                     const int i = k * GL + tl, t = tg + i;
                     float dt = 0.f, dtu = 0.f;
                     if (t < t1 && live) {
-                        const float d = ld(dp + t * a.delta.st) + bias;
+                        const float d = ld(dp + t * a.delta.v.st) + bias;
                         dt = a.softplus ? softplus(d) : d;
-                        dtu = dt * ld(up + t * a.u.st);
+                        dtu = dt * ld(up + t * a.u.v.st);
                     }
                     tok[i * WCH + wch] = make_float4(dt, dtu, 0.f, 0.f);
                 }
@@ -159,12 +159,12 @@ __global__ void __launch_bounds__(BWD_THREADS) scan_bwd_kernel(ScanBwdArgs<T> A)
                 u[k] = dt[k] = raw[k] = z[k] = dy[k] = 0.f;
                 float gy = 0.f;
                 if (t < t1 && live && nl < GL) {
-                    u[k] = ld(up + t * a.u.st);
-                    raw[k] = ld(dp + t * a.delta.st) + bias;
+                    u[k] = ld(up + t * a.u.v.st);
+                    raw[k] = ld(dp + t * a.delta.v.st) + bias;
                     dt[k] = a.softplus ? softplus(raw[k]) : raw[k];
-                    dy[k] = gy = ld(yp + t * a.dy.st);
+                    dy[k] = gy = ld(yp + t * a.dy.v.st);
                     if (zp) {
-                        z[k] = ld(zp + t * a.z.st);
+                        z[k] = ld(zp + t * a.z.v.st);
                         gy *= z[k] * sigmoid(z[k]);
                     }
                 }

@@ -210,34 +210,32 @@ int pad_states(int N) { return N <= 8 ? 8 : (N <= 16 ? 16 : (N <= 32 ? 32 : 64))
 struct ScanPlan {
     int NN, LN;         // states with padding, lanes of a channel
     int chunk, nchunk;  // tokens of a chunk
-    unsigned gx;
     size_t off_S, total;
 };
 
 long long scan_warps(const sdm_scan_dims* d, int LN) {
-    return (long long)d->B * d->G * ceil_div(d->D / d->G, SCAN_THREADS / LN) * (SCAN_THREADS / 32);
+    return (long long)d->B * d->G * ceil_div(d->D / d->G, 32 / LN);
 }
 
-// Lanes of a channel: as few as give every SM sub-partition a warp (fewer lanes share less work,
-// more lanes make more warps); then chunks of the tokens while half of the sub-partitions would
-// idle, since a second pass over the exponentials costs about as much as it gains above that.
+// Lanes of a channel: as few as give every SM sub-partition two warps (fewer lanes share less
+// work, more lanes make more warps); then chunks of the tokens while some sub-partitions would
+// idle, since a second pass over the exponentials costs more than it gains above that.
 ScanPlan scan_plan(const sdm_scan_dims* d) {
     ScanPlan p{};
     p.NN = pad_states(d->N);
     const int lo = p.NN <= 16 ? 1 : p.NN / 16, hi = p.NN == 8 ? 2 : (p.NN == 16 ? 4 : p.NN / 8);
     p.LN = lo;
-    while (p.LN < hi && scan_warps(d, p.LN) < 4 * kSms) p.LN *= 2;
+    while (p.LN < hi && scan_warps(d, p.LN) < 8 * kSms) p.LN *= 2;
     const long long warps = scan_warps(d, p.LN);
     p.chunk = std::max(1, d->T);
     p.nchunk = 1;
     if (warps <= 2 * kSms) {
-        const long long want = std::min(ceil_div(d->T, 64), 8 * kSms / warps);
+        const long long want = std::min(ceil_div(d->T, 64), 16 * kSms / warps);
         if (want > 1) {
             p.chunk = (int)(ceil_div(ceil_div(d->T, want), SCAN_TILE) * SCAN_TILE);
             p.nchunk = (int)ceil_div(d->T, p.chunk);
         }
     }
-    p.gx = (unsigned)(d->G * ceil_div(d->D / d->G, SCAN_THREADS / p.LN));
     const size_t bc = (size_t)d->B * p.nchunk * d->D;
     if (p.nchunk > 1) {
         p.off_S = up256(bc * d->N * 4);
@@ -246,14 +244,40 @@ ScanPlan scan_plan(const sdm_scan_dims* d) {
     return p;
 }
 
+// Bytes that one asynchronous copy may move of a view's rows of `row` bytes which also start at
+// multiples of `step` bytes: 16, 8, 4, or 0 where nothing is aligned enough.
+int copy_piece(const sdm_view* v, size_t es, size_t row, size_t step) {
+    const uint64_t bits = (uint64_t)(uintptr_t)v->data | (uint64_t)v->sb * es | (uint64_t)v->sh * es |
+                          (uint64_t)v->st * es | row | step;
+    return bits % 16 == 0 ? 16 : (bits % 8 == 0 ? 8 : (bits % 4 == 0 ? 4 : 0));
+}
+
+template <typename T>
+Rows<T> rows(const sdm_view* v) {
+    return Rows<T>{view<const T>(v), 0};
+}
+
+// The pieces of a walk whose warps take `ch` channels: rows of ch elements in shared memory, that
+// start at multiples of them within a group; B and C rows of NN.
+template <typename T>
+void set_pieces(ScanArgs<T>& a, const sdm_view* const (&v)[6], int ch, int NN) {
+    Rows<T>* r[6] = {&a.u, &a.delta, &a.z, &a.dy, &a.Bm, &a.Cm};
+    for (int i = 0; i < 6; ++i) {
+        if (!v[i]) continue;
+        const size_t row = (size_t)(i < 4 ? ch : NN) * sizeof(T);
+        const size_t step = i < 4 ? (size_t)(a.G > 1 ? a.D / a.G : 0) * sizeof(T) : 0;
+        r[i]->piece = copy_piece(v[i], sizeof(T), row, step);
+    }
+}
+
 template <typename T>
 ScanArgs<T> scan_args(const sdm_scan_dims* d, const sdm_view* u, const sdm_view* delta,
                       const float* A, const sdm_view* Bm, const sdm_view* Cm, const float* Dskip,
                       const sdm_view* z, const float* dt_bias, const float* state,
                       const int32_t* lens) {
     ScanArgs<T> a{};
-    a.u = view<const T>(u), a.delta = view<const T>(delta), a.z = view<const T>(z);
-    a.Bm = view<const T>(Bm), a.Cm = view<const T>(Cm);
+    a.u = rows<T>(u), a.delta = rows<T>(delta), a.z = rows<T>(z);
+    a.Bm = rows<T>(Bm), a.Cm = rows<T>(Cm);
     a.A = A, a.Dskip = Dskip, a.dt_bias = dt_bias;
     a.state = const_cast<float*>(state);
     a.lens = lens;
@@ -262,15 +286,26 @@ ScanArgs<T> scan_args(const sdm_scan_dims* d, const sdm_view* u, const sdm_view*
     return a;
 }
 
+template <typename T, int NPT, int LN, int MODE>
+sdm_status launch_walk(const ScanArgs<T>& a, int chunks, cudaStream_t s) {
+    constexpr int WCH = 32 / LN;
+    constexpr size_t smem = sizeof(ScanShared<T, NPT * LN, WCH, MODE>);
+    if (!allow_smem(scan_walk_kernel<T, NPT, LN, MODE>, smem)) return SDM_ERR_CUDA;
+    const unsigned gx = (unsigned)(a.G * ceil_div(a.D / a.G, WCH));
+    scan_walk_kernel<T, NPT, LN, MODE><<<dim3(gx, chunks, a.B), 32, smem, s>>>(a);
+    return launched();
+}
+
 template <typename T, int NPT, int LN>
-void launch_scan_t(const ScanArgs<T>& a, const ScanPlan& p, cudaStream_t s) {
-    if (p.nchunk > 1) {
-        scan_chunk_kernel<T, NPT, LN, false>
-            <<<dim3(p.gx, p.nchunk - 1, a.B), SCAN_THREADS, 0, s>>>(a);
+sdm_status launch_scan_t(ScanArgs<T> a, const sdm_view* const (&v)[6], cudaStream_t s) {
+    set_pieces(a, v, 32 / LN, NPT * LN);
+    if (a.nchunk > 1) {
+        const sdm_status e = launch_walk<T, NPT, LN, SCAN_CHUNK>(a, a.nchunk - 1, s);
+        if (e) return e;
         const long long n = (long long)a.B * a.D * a.N;
         scan_carry_kernel<T><<<(unsigned)ceil_div(n, 256), 256, 0, s>>>(a, 0);
     }
-    scan_out_kernel<T, NPT, LN><<<dim3(p.gx, p.nchunk, a.B), SCAN_THREADS, 0, s>>>(a);
+    return launch_walk<T, NPT, LN, SCAN_OUT>(a, a.nchunk, s);
 }
 
 template <typename T>
@@ -284,8 +319,8 @@ void launch_step(const ScanArgs<T>& a, int NN, cudaStream_t s) {
 }
 
 template <typename T>
-sdm_status run_scan(const sdm_scan_dims* d, ScanArgs<T> a, const sdm_view* y, void* ws,
-                    cudaStream_t s) {
+sdm_status run_scan(const sdm_scan_dims* d, ScanArgs<T> a, const sdm_view* const (&v)[6],
+                    const sdm_view* y, void* ws, cudaStream_t s) {
     a.y = view<T>(y);
     if (d->T == 1) {
         launch_step<T>(a, pad_states(d->N), s);
@@ -295,21 +330,17 @@ sdm_status run_scan(const sdm_scan_dims* d, ScanArgs<T> a, const sdm_view* y, vo
     a.chunk = p.chunk, a.nchunk = p.nchunk;
     a.E = static_cast<float*>(ws);
     a.S = reinterpret_cast<float*>(static_cast<char*>(ws) + p.off_S);
-    if (p.NN == 8) {
-        if (p.LN == 1) launch_scan_t<T, 8, 1>(a, p, s);
-        else launch_scan_t<T, 4, 2>(a, p, s);
-    } else if (p.NN == 16) {
-        if (p.LN == 1) launch_scan_t<T, 16, 1>(a, p, s);
-        else if (p.LN == 2) launch_scan_t<T, 8, 2>(a, p, s);
-        else launch_scan_t<T, 4, 4>(a, p, s);
-    } else if (p.NN == 32) {
-        if (p.LN == 2) launch_scan_t<T, 16, 2>(a, p, s);
-        else launch_scan_t<T, 8, 4>(a, p, s);
-    } else {
-        if (p.LN == 4) launch_scan_t<T, 16, 4>(a, p, s);
-        else launch_scan_t<T, 8, 8>(a, p, s);
+    switch (p.NN * 16 + p.LN) {
+        case 8 * 16 + 1: return launch_scan_t<T, 8, 1>(a, v, s);
+        case 8 * 16 + 2: return launch_scan_t<T, 4, 2>(a, v, s);
+        case 16 * 16 + 1: return launch_scan_t<T, 16, 1>(a, v, s);
+        case 16 * 16 + 2: return launch_scan_t<T, 8, 2>(a, v, s);
+        case 16 * 16 + 4: return launch_scan_t<T, 4, 4>(a, v, s);
+        case 32 * 16 + 2: return launch_scan_t<T, 16, 2>(a, v, s);
+        case 32 * 16 + 4: return launch_scan_t<T, 8, 4>(a, v, s);
+        case 64 * 16 + 4: return launch_scan_t<T, 16, 4>(a, v, s);
+        default: return launch_scan_t<T, 8, 8>(a, v, s);
     }
-    return launched();
 }
 
 struct ScanBwdPlan {
@@ -343,12 +374,14 @@ ScanBwdPlan scan_bwd_plan(const sdm_scan_dims* d) {
 }
 
 template <typename T, int LN>
-sdm_status launch_scan_bwd_t(const ScanBwdArgs<T>& A, const ScanBwdPlan& p, cudaStream_t s) {
-    const ScanArgs<T>& a = A.s;
+sdm_status launch_scan_bwd_t(const ScanBwdArgs<T>& A, const ScanBwdPlan& p,
+                             const sdm_view* const (&v)[6], cudaStream_t s) {
+    ScanArgs<T> a = A.s;
     constexpr int NN = LN * BWD_NPT, CLN = NN / 8;
     if (p.nchunk > 1) {
-        const unsigned gx = (unsigned)(a.G * ceil_div(a.D / a.G, SCAN_THREADS / CLN));
-        scan_chunk_kernel<T, 8, CLN, true><<<dim3(gx, p.nchunk, a.B), SCAN_THREADS, 0, s>>>(a);
+        set_pieces(a, v, 32 / CLN, NN);
+        const sdm_status e = launch_walk<T, 8, CLN, SCAN_CHUNK_REV>(a, p.nchunk, s);
+        if (e) return e;
         const unsigned n = (unsigned)ceil_div((long long)a.B * a.D * a.N, 256);
         scan_carry_kernel<T><<<n, 256, 0, s>>>(a, 0);
         scan_carry_kernel<T><<<n, 256, 0, s>>>(a, 1);
@@ -361,13 +394,13 @@ sdm_status launch_scan_bwd_t(const ScanBwdArgs<T>& A, const ScanBwdPlan& p, cuda
 }
 
 template <typename T>
-sdm_status run_scan_bwd(const sdm_scan_dims* d, ScanArgs<T> a, const sdm_view* dy,
+sdm_status run_scan_bwd(const sdm_scan_dims* d, ScanArgs<T> a, const sdm_view* const (&v)[6],
                         const float* dstate_end, const sdm_view* du, const sdm_view* ddelta,
                         float* dA, void* dB, void* dC, float* dDskip, const sdm_view* dz,
                         float* ddt_bias, float* dstate, void* ws, cudaStream_t s) {
     const ScanBwdPlan p = scan_bwd_plan(d);
     char* base = static_cast<char*>(ws);
-    a.dy = view<const T>(dy);
+    a.dy = rows<T>(v[3]);
     a.dstate_end = dstate_end;
     a.chunk = BWD_CHUNK, a.nchunk = p.nchunk;
     a.E = reinterpret_cast<float*>(base);
@@ -382,10 +415,10 @@ sdm_status run_scan_bwd(const sdm_scan_dims* d, ScanArgs<T> a, const sdm_view* d
     A.dstate = dstate;
     A.tiles = p.tiles, A.blocks = p.blocks;
     sdm_status e;
-    if (p.NN == 8) e = launch_scan_bwd_t<T, 2>(A, p, s);
-    else if (p.NN == 16) e = launch_scan_bwd_t<T, 4>(A, p, s);
-    else if (p.NN == 32) e = launch_scan_bwd_t<T, 8>(A, p, s);
-    else e = launch_scan_bwd_t<T, 16>(A, p, s);
+    if (p.NN == 8) e = launch_scan_bwd_t<T, 2>(A, p, v, s);
+    else if (p.NN == 16) e = launch_scan_bwd_t<T, 4>(A, p, v, s);
+    else if (p.NN == 32) e = launch_scan_bwd_t<T, 8>(A, p, v, s);
+    else e = launch_scan_bwd_t<T, 16>(A, p, v, s);
     if (e) return e;
     const long long btg = (long long)d->B * d->T * d->G;
     if (btg > 0)
@@ -520,11 +553,12 @@ sdm_status sdm_selective_scan(const sdm_scan_dims* dims, const sdm_view* u, cons
     const size_t need = sdm_selective_scan_workspace_bytes(dims);
     if (need && (!ws || ws_bytes < need)) return SDM_ERR_WORKSPACE;
     if (!aligned(ws, 16)) return SDM_ERR_ALIGN;
+    const sdm_view* const v[6] = {u, delta, z, nullptr, Bm, Cm};
     if (dims->x_dtype == SDM_BF16)
         return run_scan<bf16>(dims, scan_args<bf16>(dims, u, delta, A, Bm, Cm, Dskip, z, dt_bias,
-                                                    state, lens), y, ws, stream);
+                                                    state, lens), v, y, ws, stream);
     return run_scan<float>(dims, scan_args<float>(dims, u, delta, A, Bm, Cm, Dskip, z, dt_bias,
-                                                  state, lens), y, ws, stream);
+                                                  state, lens), v, y, ws, stream);
 }
 
 size_t sdm_selective_scan_backward_workspace_bytes(const sdm_scan_dims* dims) {
@@ -559,14 +593,15 @@ sdm_status sdm_selective_scan_backward(
     if (!ws || ws_bytes < sdm_selective_scan_backward_workspace_bytes(dims))
         return SDM_ERR_WORKSPACE;
     if (!aligned(ws, 16)) return SDM_ERR_ALIGN;
+    const sdm_view* const v[6] = {u, delta, z, dy, Bm, Cm};
     if (dims->x_dtype == SDM_BF16)
         return run_scan_bwd<bf16>(dims, scan_args<bf16>(dims, u, delta, A, Bm, Cm, Dskip, z,
                                                         dt_bias, state, lens),
-                                  dy, dstate_end, du, ddelta, dA, dB, dC, dDskip, dz, ddt_bias,
+                                  v, dstate_end, du, ddelta, dA, dB, dC, dDskip, dz, ddt_bias,
                                   dstate, ws, stream);
     return run_scan_bwd<float>(dims, scan_args<float>(dims, u, delta, A, Bm, Cm, Dskip, z, dt_bias,
                                                       state, lens),
-                               dy, dstate_end, du, ddelta, dA, dB, dC, dDskip, dz, ddt_bias, dstate,
+                               v, dstate_end, du, ddelta, dA, dB, dC, dDskip, dz, ddt_bias, dstate,
                                ws, stream);
 }
 

@@ -78,10 +78,29 @@ SDM_DEV float exp2_fast(float x) {
 
 SDM_DEV float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
 
-// log(1 + e^x), the identity above 20 (where it differs by less than half an fp32 step).  Below
-// it, log1p keeps the relative accuracy of small steps, and expf rather than __expf, whose error
-// grows with |x|: a step's relative error goes into every state and gradient behind it.
-SDM_DEV float softplus(float x) { return x > 20.f ? x : log1pf(expf(x)); }
+// log(1 + e^x) = max(x, 0) + log(1 + e), e = e^-|x| <= 1, to a few units in the last place: a
+// step's relative error goes into every state and gradient behind it, so small steps (x << 0)
+// keep theirs.  log(1 + e) = 2 atanh(w), w = e / (2 + e) <= 1/3, by its Taylor series (the first
+// term left out is below 2^-24 of the sum); the rounding of |x| log2(e), which would cost e up to
+// |x| 2^-24, is put back to first order.
+SDM_DEV float softplus(float x) {
+    float a = fabsf(x);
+    if (a > 128.f) a = 128.f;  // e is 0 there; a NaN stays
+    const float p = a * kLog2e;
+    const float lo = fmaf(a, kLog2e, -p) + a * 1.925963033500e-8f;  // log2(e) - its fp32 value
+    float e = exp2_fast(-p);
+    e = fmaf(e, -0.69314718f * lo, e);
+    const float w = __fdividef(e, 2.f + e), q = w * w;
+    float s = 2.f / 15.f;
+    s = fmaf(s, q, 2.f / 13.f);
+    s = fmaf(s, q, 2.f / 11.f);
+    s = fmaf(s, q, 2.f / 9.f);
+    s = fmaf(s, q, 2.f / 7.f);
+    s = fmaf(s, q, 2.f / 5.f);
+    s = fmaf(s, q, 2.f / 3.f);
+    s = fmaf(s * q, w, 2.f * w);
+    return fmaxf(x, 0.f) + s;
+}
 
 SDM_DEV int clamp_len(const int* lens, int b, int T) {
     if (!lens) return T;
