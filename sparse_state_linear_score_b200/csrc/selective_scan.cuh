@@ -53,32 +53,6 @@ struct ScanArgs {
     int chunk, nchunk;  // tokens of a chunk
 };
 
-// ---- two fp32 at a time --------------------------------------------------------------------
-typedef unsigned long long f32x2;
-SDM_DEV f32x2 pack2(float lo, float hi) {
-    f32x2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-SDM_DEV void unpack2(f32x2 v, float& lo, float& hi) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-SDM_DEV f32x2 mul2(f32x2 a, f32x2 b) {
-    f32x2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-SDM_DEV f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
-    f32x2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-SDM_DEV f32x2 exp2_pair(f32x2 x) {
-    float lo, hi;
-    unpack2(x, lo, hi);
-    return pack2(exp2_fast(lo), exp2_fast(hi));
-}
-
 // Sums v[i], i < 8, over LN neighbouring lanes; lane l of them ends with token k*LN + l in v[k].
 template <int LN>
 SDM_DEV void spread_sum(float (&v)[SCAN_GRP], int nl) {
@@ -97,40 +71,76 @@ SDM_DEV void spread_sum(float (&v)[SCAN_GRP], int nl) {
     }
 }
 
-// Copies W elements of each of TILE rows (tokens t.. of a sequence, zero from t1 on and behind
-// `cols`) to s[TILE][W], by the warp.  Pieces of 16, 8 or 4 bytes go asynchronously.
+// Copies W elements of each of TILE rows of a view (tokens t.., zero from t1 on and behind
+// `cols`) to shared memory, by the warp, tile after tile.  Where the rows allow whole pieces of
+// PIECE bytes a lane copies the same pieces of every tile and keeps their address, so that a piece
+// costs a comparison, an addition and the copy.
 template <typename T, int W, int TILE>
-SDM_DEV void rows_to_smem(const T* p, long long stride, int piece, int t, int t1, int cols, T* s) {
-    const int lane = threadIdx.x & 31;
-    if (piece) {
-        const int per = W * (int)sizeof(T) / piece;  // pieces of a row, a power of two
-        const int sh = __ffs(per) - 1;
-        for (int i = lane; i < TILE * per; i += 32) {
-            const int r = i >> sh, k = i & (per - 1);
-            int bytes = t + r < t1 ? cols * (int)sizeof(T) - k * piece : 0;
-            bytes = bytes < 0 ? 0 : (bytes > piece ? piece : bytes);
-            const char* src = reinterpret_cast<const char*>(p);
-            if (bytes > 0) src = reinterpret_cast<const char*>(p + (t + r) * stride) + k * piece;
-            const uint32_t dst = (uint32_t)__cvta_generic_to_shared(s + r * W) + k * piece;
-            if (piece == 16)
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-                             "r"(bytes) : "memory");
-            else if (piece == 8)
-                asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src),
-                             "r"(bytes) : "memory");
-            else
-                asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
-                             "r"(bytes) : "memory");
-        }
-    } else {
-        for (int i = lane; i < TILE * W; i += 32) {
-            const int r = i / W, k = i % W;
-            T v = T(0.f);
-            if (t + r < t1 && k < cols) v = p[(t + r) * stride + k];
-            s[i] = v;
+struct RowCopy {
+    static constexpr int ROW = W * (int)sizeof(T), PIECE = ROW < 16 ? ROW : 16, PER = ROW / PIECE;
+    static constexpr int ITER = (TILE * PER + 31) / 32, RSTEP = 32 / PER;  // rows between a lane's pieces
+    static_assert(PER <= 32 && (PER & (PER - 1)) == 0, "pieces of a row");
+    const T* p;           // element (t0, 0)
+    const char* next;     // the lane's first piece of the next tile
+    long long stride;
+    int piece, cols, bytes;
+    SDM_DEV void init(const Rows<T>& r, long long at, int t0, int columns) {
+        const int lane = threadIdx.x & 31;
+        stride = r.v.st;
+        p = r.v.p + at + t0 * stride;
+        piece = r.piece;
+        cols = columns;
+        const int k = lane % PER * PIECE;
+        next = reinterpret_cast<const char*>(p + lane / PER * stride) + k;
+        bytes = lane < TILE * PER ? min(max(cols * (int)sizeof(T) - k, 0), PIECE) : 0;
+    }
+    template <int BYTES>
+    SDM_DEV static void copy(uint32_t dst, const void* src, int n) {
+        if (BYTES == 16)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
+                         : "memory");
+        else
+            asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src), "r"(n),
+                         "n"(BYTES)
+                         : "memory");
+    }
+    // Rows that allow smaller pieces only (or, of bf16 at odd addresses, none).
+    template <int BYTES>
+    SDM_DEV void small(int first, int left, T* s) const {
+        constexpr int E = BYTES / (int)sizeof(T);
+        for (int i = threadIdx.x & 31; i < TILE * W / E; i += 32) {
+            const int r = i * E / W, k = i * E % W;
+            const int n = r < left ? min(max((cols - k) * (int)sizeof(T), 0), BYTES) : 0;
+            copy<BYTES>((uint32_t)__cvta_generic_to_shared(s + i * E),
+                        n ? p + (first + r) * stride + k : p, n);
         }
     }
-}
+    // The tile that starts `first` tokens behind t0; `left` tokens remain from there.
+    SDM_DEV void fetch(int first, int left, T* s) {
+        if (piece >= PIECE) {
+            const int lane = threadIdx.x & 31;
+            const uint32_t dst = (uint32_t)__cvta_generic_to_shared(s) + lane * PIECE;
+#pragma unroll
+            for (int i = 0; i < ITER; ++i) {
+                if (TILE * PER < 32 && lane >= TILE * PER) break;
+                copy<PIECE>(dst + i * 32 * PIECE, next + i * RSTEP * stride * (long long)sizeof(T),
+                            lane / PER + i * RSTEP < left ? bytes : 0);
+            }
+            next += TILE * stride * (long long)sizeof(T);
+        } else if (piece == 8) {
+            small<8>(first, left, s);
+        } else if (piece == 4) {
+            small<4>(first, left, s);
+        } else {
+            for (int i = threadIdx.x & 31; i < TILE * W; i += 32) {
+                const int r = i / W, k = i % W;
+                T v = T(0.f);
+                if (r < left && k < cols) v = p[(first + r) * stride + k];
+                s[i] = v;
+            }
+        }
+    }
+};
 SDM_DEV void async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 SDM_DEV void async_wait() {
@@ -171,16 +181,18 @@ struct ScanLane {
         n0 = nl * NPT;
         b = blockIdx.z;
     }
+    static constexpr int PC = NPT < 4 ? NPT : 4;
     SDM_DEV void load(const float* p, int N, float (&v)[NPT]) const {  // p: the channel's row
-        if (N % 4 == 0) {  // rows of whole 16-byte pieces
+        if (N % 4 == 0) {  // rows of whole pieces
 #pragma unroll
-            for (int i = 0; i < NPT; i += 4)
-                if (live && n0 + i < N) {
-                    const float4 x = *reinterpret_cast<const float4*>(p + n0 + i);
-                    v[i] = x.x, v[i + 1] = x.y, v[i + 2] = x.z, v[i + 3] = x.w;
-                } else {
-                    v[i] = v[i + 1] = v[i + 2] = v[i + 3] = 0.f;
-                }
+            for (int i = 0; i < NPT; i += PC) {
+                float x[PC];
+#pragma unroll
+                for (int k = 0; k < PC; ++k) x[k] = 0.f;
+                if (live && n0 + i < N) Vec<PC>::load(p + n0 + i, x);
+#pragma unroll
+                for (int k = 0; k < PC; ++k) v[i + k] = x[k];
+            }
         } else {
 #pragma unroll
             for (int i = 0; i < NPT; ++i) v[i] = live && n0 + i < N ? p[n0 + i] : 0.f;
@@ -190,10 +202,12 @@ struct ScanLane {
         if (!live) return;
         if (N % 4 == 0) {
 #pragma unroll
-            for (int i = 0; i < NPT; i += 4)
-                if (n0 + i < N)
-                    *reinterpret_cast<float4*>(p + n0 + i) =
-                        make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+            for (int i = 0; i < NPT; i += PC) {
+                float x[PC];
+#pragma unroll
+                for (int k = 0; k < PC; ++k) x[k] = v[i + k];
+                if (n0 + i < N) Vec<PC>::store(p + n0 + i, x);
+            }
         } else {
 #pragma unroll
             for (int i = 0; i < NPT; ++i)
@@ -213,8 +227,9 @@ template <typename T, int NN, int WCH, int MODE>
 struct ScanShared {
     ScanStage<T, NN, WCH, MODE> st[SCAN_STAGES];
     float B[SCAN_TILE * NN], C[SCAN_TILE * NN];  // the tile's, of bf16 rows
-    float2 tok[SCAN_TILE * WCH];                 // a token's step and step * u
-    float y[SCAN_TILE * WCH];                    // its sum C h, or (gradient) the gated dy
+    ulonglong2 tok[SCAN_TILE * WCH];             // a token's step twice, its step * u twice
+    f32x2 g[MODE == SCAN_CHUNK_REV ? SCAN_TILE * WCH : 2];  // its gated dy twice
+    float y[MODE == SCAN_OUT ? SCAN_TILE * 32 : 4];         // each lane's share of its sum C h
 };
 
 // The walk over a chunk.  SCAN_OUT: its outputs from the start state (and the end state where the
@@ -223,7 +238,9 @@ struct ScanShared {
 // sum_t (prod_{s<=t} a_s) C_t dy_t.
 template <typename T, int NPT, int LN, int MODE>
 __global__ void __launch_bounds__(32) scan_walk_kernel(ScanArgs<T> a) {
-    constexpr int NN = NPT * LN, NP = NPT / 2, WCH = 32 / LN, ITEMS = SCAN_TILE * WCH / 32;
+    constexpr int NN = NPT * LN, NP = NPT / 2, WCH = 32 / LN;
+    constexpr int PAIRS = SCAN_TILE * WCH / 64;  // of (token, channel pair) a lane
+    constexpr int SB = NP >= 8 ? 2 : (NP >= 4 ? 4 : 8);  // tokens whose decays are computed ahead
     constexpr bool OUT = MODE == SCAN_OUT, REV = MODE == SCAN_CHUNK_REV;
     extern __shared__ __align__(16) char smem[];
     using Shared = ScanShared<T, NN, WCH, MODE>;
@@ -234,27 +251,28 @@ __global__ void __launch_bounds__(32) scan_walk_kernel(ScanArgs<T> a) {
     const int t0 = blockIdx.y * a.chunk, t1 = min(t0 + a.chunk, len);
     if (OUT && t0 >= len && blockIdx.y > 0) return;
     const bool gate = a.z.v.p && (OUT || REV);
-    const T* up = a.u.v.p + L.b * a.u.v.sb + L.c0;
-    const T* dp = a.delta.v.p + L.b * a.delta.v.sb + L.c0;
-    const T* zp = gate ? a.z.v.p + L.b * a.z.v.sb + L.c0 : nullptr;
-    const T* gp = REV ? a.dy.v.p + L.b * a.dy.v.sb + L.c0 : nullptr;
-    const T* Bp = a.Bm.v.p + L.b * a.Bm.v.sb + L.g * a.Bm.v.sh;
-    const T* Cp = a.Cm.v.p + L.b * a.Cm.v.sb + L.g * a.Cm.v.sh;
+    RowCopy<T, WCH, SCAN_TILE> cu, cd, cz, cg;
+    RowCopy<T, NN, SCAN_TILE> cB, cC;
+    cu.init(a.u, L.b * a.u.v.sb + L.c0, t0, L.cols);
+    cd.init(a.delta, L.b * a.delta.v.sb + L.c0, t0, L.cols);
+    if (gate) cz.init(a.z, L.b * a.z.v.sb + L.c0, t0, L.cols);
+    if (REV) cg.init(a.dy, L.b * a.dy.v.sb + L.c0, t0, L.cols);
+    cB.init(a.Bm, L.b * a.Bm.v.sb + L.g * a.Bm.v.sh, t0, a.N);
+    if (OUT || REV) cC.init(a.Cm, L.b * a.Cm.v.sb + L.g * a.Cm.v.sh, t0, a.N);
     auto fetch = [&](int tile) {
-        const int t = t0 + tile * SCAN_TILE;
-        if (t < t1) {
+        const int first = tile * SCAN_TILE, left = t1 - t0 - first;
+        if (left > 0) {
             auto& s = sh.st[tile % SCAN_STAGES];
-            rows_to_smem<T, WCH, SCAN_TILE>(up, a.u.v.st, a.u.piece, t, t1, L.cols, s.u);
-            rows_to_smem<T, WCH, SCAN_TILE>(dp, a.delta.v.st, a.delta.piece, t, t1, L.cols, s.d);
-            if (gate) rows_to_smem<T, WCH, SCAN_TILE>(zp, a.z.v.st, a.z.piece, t, t1, L.cols, s.z);
-            if (REV) rows_to_smem<T, WCH, SCAN_TILE>(gp, a.dy.v.st, a.dy.piece, t, t1, L.cols, s.dy);
-            rows_to_smem<T, NN, SCAN_TILE>(Bp, a.Bm.v.st, a.Bm.piece, t, t1, a.N, s.B);
-            if (OUT || REV)
-                rows_to_smem<T, NN, SCAN_TILE>(Cp, a.Cm.v.st, a.Cm.piece, t, t1, a.N, s.C);
+            cu.fetch(first, left, s.u);
+            cd.fetch(first, left, s.d);
+            if (gate) cz.fetch(first, left, s.z);
+            if (REV) cg.fetch(first, left, s.dy);
+            cB.fetch(first, left, s.B);
+            if (OUT || REV) cC.fetch(first, left, s.C);
         }
         async_commit();
     };
-#pragma unroll
+#pragma unroll 1
     for (int i = 0; i < SCAN_STAGES - 1; ++i) fetch(i);
 
     float tmp[NPT];
@@ -263,8 +281,8 @@ __global__ void __launch_bounds__(32) scan_walk_kernel(ScanArgs<T> a) {
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
         A2[i] = pack2(tmp[2 * i] * kLog2e, tmp[2 * i + 1] * kLog2e);
-        r[i] = pack2(0.f, 0.f);
-        P[i] = pack2(1.f, 1.f);
+        r[i] = dup2(0.f);
+        P[i] = dup2(1.f);
     }
 #pragma unroll
     for (int i = 0; i < NPT; ++i) tmp[i] = 0.f;
@@ -275,13 +293,15 @@ __global__ void __launch_bounds__(32) scan_walk_kernel(ScanArgs<T> a) {
 #pragma unroll
     for (int i = 0; i < NP; ++i) h[i] = pack2(tmp[2 * i], tmp[2 * i + 1]);
 
-    // before and after the walk a lane looks after channel lane % WCH, every (32/WCH)-th token
-    const int ic = lane % WCH, ig = L.c0 + (ic < L.cols ? ic : 0);
-    const float bias = a.dt_bias ? a.dt_bias[ig] : 0.f;
-    const float skip = OUT && a.Dskip ? a.Dskip[ig] : 0.f;
+    // before and after the walk a lane looks after two channels, of every (64/WCH)-th token
+    const int ic = 2 * (lane % (WCH / 2));
+    const int i0 = L.c0 + (ic < L.cols ? ic : 0), i1 = L.c0 + (ic + 1 < L.cols ? ic + 1 : 0);
+    const f32x2 bias = a.dt_bias ? pack2(a.dt_bias[i0], a.dt_bias[i1]) : dup2(0.f);
+    const f32x2 skip = OUT && a.Dskip ? pack2(a.Dskip[i0], a.Dskip[i1]) : dup2(0.f);
     T* yp = OUT ? a.y.p + L.b * a.y.sb + L.c0 + ic : nullptr;
-    float steps = 0.f;
-    const float2* tok = sh.tok + lane / LN;
+    const bool pair = OUT && ic + 1 < L.cols && ((uintptr_t)yp % (2 * sizeof(T))) == 0 && a.y.st % 2 == 0;
+    f32x2 steps = dup2(0.f);
+    const ulonglong2* tok = sh.tok + lane / LN;
 
     for (int tile = 0; t0 + tile * SCAN_TILE < t1; ++tile) {
         const int tt = t0 + tile * SCAN_TILE;
@@ -290,75 +310,117 @@ __global__ void __launch_bounds__(32) scan_walk_kernel(ScanArgs<T> a) {
         fetch(tile + SCAN_STAGES - 1);  // into the stage that the tile before this one used
         const auto& s = sh.st[tile % SCAN_STAGES];
 #pragma unroll
-        for (int k = 0; k < ITEMS; ++k) {
-            const int e = lane + 32 * k, t = tt + e / WCH;
-            float step = ld(s.d + e) + bias;
-            if (a.softplus) step = softplus(step);
-            if (t >= t1) step = 0.f;  // behind the sequence: the state stays
-            sh.tok[e] = make_float2(step, step * ld(s.u + e));
-            if (!OUT) steps += step;
+        for (int k = 0; k < PAIRS; ++k) {
+            const int e = 2 * (lane + 32 * k);
+            float d[2], u[2];
+            Vec<2>::load(s.d + e, d);
+            Vec<2>::load(s.u + e, u);
+            f32x2 st2 = add2(pack2(d[0], d[1]), bias);
+            if (a.softplus) st2 = softplus2(st2);
+            if (tt + e / WCH >= t1) st2 = dup2(0.f);  // behind the sequence: the state stays
+            const f32x2 su2 = mul2(st2, pack2(u[0], u[1]));
+            float s0, s1, w0, w1;
+            unpack2(st2, s0, s1);
+            unpack2(su2, w0, w1);
+            sh.tok[e] = make_ulonglong2(dup2(s0), dup2(w0));
+            sh.tok[e + 1] = make_ulonglong2(dup2(s1), dup2(w1));
+            if (!OUT) steps = add2(steps, st2);
             if (REV) {
-                float g = ld(s.dy + e);
+                float g[2];
+                Vec<2>::load(s.dy + e, g);
+                f32x2 g2 = pack2(g[0], g[1]);
                 if (gate) {
-                    const float z = ld(s.z + e);
-                    g *= z * sigmoid(z);
+                    float z[2];
+                    Vec<2>::load(s.z + e, z);
+                    g2 = mul2(g2, silu2(pack2(z[0], z[1])));
                 }
-                sh.y[e] = g;
+                unpack2(g2, g[0], g[1]);
+                sh.g[e] = dup2(g[0]);
+                sh.g[e + 1] = dup2(g[1]);
             }
         }
-        const float* Bs = rows_as_float<T, SCAN_TILE * NN>(s.B, sh.B);
+        const float* Bs = rows_as_float<T, SCAN_TILE * NN>(s.B, sh.B) + L.n0;
         const float* Cs = nullptr;
-        if (OUT || REV) Cs = rows_as_float<T, SCAN_TILE * NN>(s.C, sh.C);
+        if (OUT || REV) Cs = rows_as_float<T, SCAN_TILE * NN>(s.C, sh.C) + L.n0;
         __syncwarp();
+        float ysh[OUT ? SCAN_TILE : 1];  // stored behind the walk: its loads can be moved up
 #pragma unroll
-        for (int gq = 0; gq < SCAN_TILE / SCAN_GRP; ++gq) {
-            float y[SCAN_GRP];
+        for (int q0 = 0; q0 < SCAN_TILE; q0 += SB) {
+            f32x2 dec[SB][NP], in[SB][NP];
 #pragma unroll
-            for (int i = 0; i < SCAN_GRP; ++i) {
-                const int q = gq * SCAN_GRP + i;
-                const float2 x = tok[q * WCH];
-                const f32x2 d2 = pack2(x.x, x.x), e2 = pack2(x.y, x.y);
-                const f32x2* Br = reinterpret_cast<const f32x2*>(Bs + q * NN + L.n0);
-                const f32x2* Cr = reinterpret_cast<const f32x2*>(Cs + q * NN + L.n0);
-                f32x2 acc = pack2(0.f, 0.f), g2;
-                if (REV) {
-                    const float g = sh.y[q * WCH + lane / LN];
-                    g2 = pack2(g, g);
-                }
+            for (int i = 0; i < SB; ++i) {
+                const ulonglong2 x = tok[(q0 + i) * WCH];
+                const f32x2* Br = reinterpret_cast<const f32x2*>(Bs + (q0 + i) * NN);
 #pragma unroll
                 for (int p = 0; p < NP; ++p) {
-                    const f32x2 dec = exp2_pair(mul2(d2, A2[p]));
-                    h[p] = fma2(dec, h[p], mul2(e2, Br[p]));
-                    if (OUT) acc = fma2(h[p], Cr[p], acc);
+                    dec[i][p] = exp2_pair(mul2(x.x, A2[p]));
+                    in[i][p] = mul2(x.y, Br[p]);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < SB; ++i) {
+                const f32x2* Cr = reinterpret_cast<const f32x2*>(Cs + (q0 + i) * NN);
+                f32x2 acc = dup2(0.f), g2;
+                if (REV) g2 = sh.g[(q0 + i) * WCH + lane / LN];
+#pragma unroll
+                for (int p = 0; p < NP; ++p) {
+                    h[p] = fma2(dec[i][p], h[p], in[i][p]);
+                    if (OUT) acc = p == 0 ? mul2(h[p], Cr[p]) : fma2(h[p], Cr[p], acc);
                     if (REV) {
-                        P[p] = mul2(P[p], dec);
+                        P[p] = mul2(P[p], dec[i][p]);
                         r[p] = fma2(P[p], mul2(g2, Cr[p]), r[p]);
                     }
                 }
                 if (OUT) {
                     float lo, hi;
                     unpack2(acc, lo, hi);
-                    y[i] = lo + hi;
+                    ysh[q0 + i] = lo + hi;
                 }
             }
-            if (OUT) {
-                spread_sum<LN>(y, L.nl);
+        }
+        if (OUT) {
 #pragma unroll
-                for (int k = 0; k < SCAN_GRP / LN; ++k)
-                    sh.y[(gq * SCAN_GRP + k * LN + L.nl) * WCH + lane / LN] = y[k];
-            }
+            for (int q = 0; q < SCAN_TILE; ++q) sh.y[q * 32 + lane] = ysh[q];
         }
         __syncwarp();
         if (OUT) {
 #pragma unroll
-            for (int k = 0; k < ITEMS; ++k) {
-                const int e = lane + 32 * k, t = tt + e / WCH;
-                float v = fmaf(skip, ld(s.u + e), sh.y[e]);
-                if (gate) {
-                    const float z = ld(s.z + e);
-                    v *= z * sigmoid(z);
+            for (int k = 0; k < PAIRS; ++k) {
+                const int e = 2 * (lane + 32 * k), t = tt + e / WCH;
+                float y[2], u[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {  // the shares of the channel's lanes
+                    const float* sy = sh.y + (e + j) * LN;
+                    if (LN == 1) {
+                        y[j] = sy[0];
+                    } else if (LN == 2) {
+                        y[j] = sy[0] + sy[1];
+                    } else {
+                        y[j] = 0.f;
+#pragma unroll
+                        for (int l = 0; l < LN; l += 4) {
+                            const float4 v = *reinterpret_cast<const float4*>(sy + l);
+                            y[j] += (v.x + v.y) + (v.z + v.w);
+                        }
+                    }
                 }
-                if (t < t1 && ic < L.cols) st(yp + t * a.y.st, v);
+                Vec<2>::load(s.u + e, u);
+                f32x2 v = fma2(skip, pack2(u[0], u[1]), pack2(y[0], y[1]));
+                if (gate) {
+                    float z[2];
+                    Vec<2>::load(s.z + e, z);
+                    v = mul2(v, silu2(pack2(z[0], z[1])));
+                }
+                unpack2(v, y[0], y[1]);
+                if (t < t1) {
+                    T* o = yp + t * a.y.st;
+                    if (pair) {
+                        Vec<2>::store(o, y);
+                    } else {
+                        if (ic < L.cols) st(o, y[0]);
+                        if (ic + 1 < L.cols) st(o + 1, y[1]);
+                    }
+                }
             }
         }
     }
@@ -377,9 +439,18 @@ __global__ void __launch_bounds__(32) scan_walk_kernel(ScanArgs<T> a) {
             for (int i = 0; i < NP; ++i) unpack2(r[i], tmp[2 * i], tmp[2 * i + 1]);
             L.store(a.R + at * a.N, a.N, tmp);
         }
+        float s0, s1;
+        unpack2(steps, s0, s1);
 #pragma unroll
-        for (int m = WCH; m < 32; m <<= 1) steps += __shfl_xor_sync(0xffffffffu, steps, m);
-        if (lane < L.cols) a.S[((long long)L.b * a.nchunk + blockIdx.y) * a.D + L.c0 + lane] = steps;
+        for (int m = WCH / 2; m < 32; m <<= 1) {
+            s0 += __shfl_xor_sync(0xffffffffu, s0, m);
+            s1 += __shfl_xor_sync(0xffffffffu, s1, m);
+        }
+        if (lane < WCH / 2) {
+            float* S = a.S + ((long long)L.b * a.nchunk + blockIdx.y) * a.D + L.c0;
+            if (ic < L.cols) S[ic] = s0;
+            if (ic + 1 < L.cols) S[ic + 1] = s1;
+        }
     }
 }
 

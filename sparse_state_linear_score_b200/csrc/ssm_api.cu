@@ -223,7 +223,7 @@ long long scan_warps(const sdm_scan_dims* d, int LN) {
 ScanPlan scan_plan(const sdm_scan_dims* d) {
     ScanPlan p{};
     p.NN = pad_states(d->N);
-    const int lo = p.NN <= 16 ? 1 : p.NN / 16, hi = p.NN == 8 ? 2 : (p.NN == 16 ? 4 : p.NN / 8);
+    const int lo = p.NN <= 16 ? 1 : p.NN / 16, hi = p.NN == 8 ? 4 : 8;
     p.LN = lo;
     while (p.LN < hi && scan_warps(d, p.LN) < 8 * kSms) p.LN *= 2;
     const long long warps = scan_warps(d, p.LN);
@@ -333,11 +333,14 @@ sdm_status run_scan(const sdm_scan_dims* d, ScanArgs<T> a, const sdm_view* const
     switch (p.NN * 16 + p.LN) {
         case 8 * 16 + 1: return launch_scan_t<T, 8, 1>(a, v, s);
         case 8 * 16 + 2: return launch_scan_t<T, 4, 2>(a, v, s);
+        case 8 * 16 + 4: return launch_scan_t<T, 2, 4>(a, v, s);
         case 16 * 16 + 1: return launch_scan_t<T, 16, 1>(a, v, s);
         case 16 * 16 + 2: return launch_scan_t<T, 8, 2>(a, v, s);
         case 16 * 16 + 4: return launch_scan_t<T, 4, 4>(a, v, s);
+        case 16 * 16 + 8: return launch_scan_t<T, 2, 8>(a, v, s);
         case 32 * 16 + 2: return launch_scan_t<T, 16, 2>(a, v, s);
         case 32 * 16 + 4: return launch_scan_t<T, 8, 4>(a, v, s);
+        case 32 * 16 + 8: return launch_scan_t<T, 4, 8>(a, v, s);
         case 64 * 16 + 4: return launch_scan_t<T, 16, 4>(a, v, s);
         default: return launch_scan_t<T, 8, 8>(a, v, s);
     }

@@ -69,6 +69,24 @@ struct Vec<4> {
     }
 };
 
+template <>
+struct Vec<2> {
+    SDM_DEV static void load(const float* p, float (&v)[2]) {
+        const float2 x = *reinterpret_cast<const float2*>(p);
+        v[0] = x.x, v[1] = x.y;
+    }
+    SDM_DEV static void load(const bf16* p, float (&v)[2]) {
+        const uint32_t x = *reinterpret_cast<const uint32_t*>(p);
+        v[0] = bf16_lo(x), v[1] = bf16_hi(x);
+    }
+    SDM_DEV static void store(float* p, const float (&v)[2]) {
+        *reinterpret_cast<float2*>(p) = make_float2(v[0], v[1]);
+    }
+    SDM_DEV static void store(bf16* p, const float (&v)[2]) {
+        *reinterpret_cast<uint32_t*>(p) = pack_bf16(v[0], v[1]);
+    }
+};
+
 // 2^x (ex2.approx: relative error about 2^-22; 0 below the normal range).
 SDM_DEV float exp2_fast(float x) {
     float y;
@@ -78,28 +96,88 @@ SDM_DEV float exp2_fast(float x) {
 
 SDM_DEV float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
 
+// ---- two fp32 at a time --------------------------------------------------------------------
+typedef unsigned long long f32x2;
+SDM_DEV f32x2 pack2(float lo, float hi) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+SDM_DEV f32x2 dup2(float x) { return pack2(x, x); }
+SDM_DEV void unpack2(f32x2 v, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+SDM_DEV f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+SDM_DEV f32x2 add2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+SDM_DEV f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+SDM_DEV f32x2 exp2_pair(f32x2 x) {
+    float lo, hi;
+    unpack2(x, lo, hi);
+    return pack2(exp2_fast(lo), exp2_fast(hi));
+}
+SDM_DEV f32x2 rcp_pair(f32x2 x) {  // rcp.approx: one unit in the last place
+    float lo, hi, a, b;
+    unpack2(x, lo, hi);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(a) : "f"(lo));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(b) : "f"(hi));
+    return pack2(a, b);
+}
+SDM_DEV float min_nan(float a, float b) {  // a NaN stays
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+SDM_DEV float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// x sigmoid(x) of two values.  Below -126 ln 2 the exponential passes rcp's range: the result is
+// then 0 where it is above -2^-118.
+SDM_DEV f32x2 silu2(f32x2 x) {
+    const f32x2 e = exp2_pair(mul2(x, dup2(-kLog2e)));
+    return mul2(x, rcp_pair(add2(e, dup2(1.f))));
+}
+
 // log(1 + e^x) = max(x, 0) + log(1 + e), e = e^-|x| <= 1, to a few units in the last place: a
 // step's relative error goes into every state and gradient behind it, so small steps (x << 0)
-// keep theirs.  log(1 + e) = 2 atanh(w), w = e / (2 + e) <= 1/3, by its Taylor series (the first
-// term left out is below 2^-24 of the sum); the rounding of |x| log2(e), which would cost e up to
-// |x| 2^-24, is put back to first order.
+// keep theirs.  log(1 + e) = 2 atanh(w), w = e / (2 + e) <= 1/3; 2 atanh(w) / w is a polynomial of
+// degree 4 in w^2, fitted at Chebyshev nodes (relative error 4e-9).  The rounding of
+// |x| log2(e), which would cost e up to |x| 2^-24, is put back to first order.
+SDM_DEV f32x2 softplus2(f32x2 x) {
+    float x0, x1;
+    unpack2(x, x0, x1);
+    const f32x2 a = pack2(min_nan(fabsf(x0), 128.f), min_nan(fabsf(x1), 128.f));  // e is 0 there
+    const f32x2 p = mul2(a, dup2(-kLog2e));
+    f32x2 lo = fma2(a, dup2(kLog2e), p);
+    lo = fma2(a, dup2(1.925963033500e-8f), lo);  // log2(e) - its fp32 value
+    f32x2 e = exp2_pair(p);
+    e = fma2(e, mul2(lo, dup2(-0.69314718f)), e);
+    const f32x2 w = mul2(e, rcp_pair(add2(e, dup2(2.f)))), q = mul2(w, w);
+    f32x2 s = fma2(dup2(0.2817465662956238f), q, dup2(0.2796141803264618f));
+    s = fma2(s, q, dup2(0.40024852752685547f));
+    s = fma2(s, q, dup2(0.6666631698608398f));
+    s = fma2(s, q, dup2(2.f));
+    s = mul2(s, w);
+    return add2(pack2(max_nan(x0, 0.f), max_nan(x1, 0.f)), s);
+}
 SDM_DEV float softplus(float x) {
-    float a = fabsf(x);
-    if (a > 128.f) a = 128.f;  // e is 0 there; a NaN stays
-    const float p = a * kLog2e;
-    const float lo = fmaf(a, kLog2e, -p) + a * 1.925963033500e-8f;  // log2(e) - its fp32 value
-    float e = exp2_fast(-p);
-    e = fmaf(e, -0.69314718f * lo, e);
-    const float w = __fdividef(e, 2.f + e), q = w * w;
-    float s = 2.f / 15.f;
-    s = fmaf(s, q, 2.f / 13.f);
-    s = fmaf(s, q, 2.f / 11.f);
-    s = fmaf(s, q, 2.f / 9.f);
-    s = fmaf(s, q, 2.f / 7.f);
-    s = fmaf(s, q, 2.f / 5.f);
-    s = fmaf(s, q, 2.f / 3.f);
-    s = fmaf(s * q, w, 2.f * w);
-    return fmaxf(x, 0.f) + s;
+    float lo, hi;
+    unpack2(softplus2(dup2(x)), lo, hi);
+    return lo;
 }
 
 SDM_DEV int clamp_len(const int* lens, int b, int T) {
