@@ -9,10 +9,10 @@
 // neighbouring lanes a channel, and products and multiply-adds go two states at a time (f32x2).
 //
 // A warp works alone, on 32/LN channels of one sequence, in tiles of 16 tokens: cp.async brings the
-// next three tiles' activations to shared memory; what a token needs once a channel (softplus,
-// before; gate and rounding, after) is spread over all lanes, one token and channel each; between
-// the two every lane walks the tile's tokens with its states.  One warp a block, so that the SMs
-// get equal numbers of them.
+// next tiles' activations to shared memory; what a token needs once a channel (softplus, before;
+// gate and rounding, after) is spread over all lanes, by token and channel pair; between the two
+// every lane walks the tile's tokens with its states.  One warp a block, so that the SMs get equal
+// numbers of them.
 //
 // Where the channels alone do not fill the GPU the tokens are split into chunks: the decay over a
 // chunk is exp(A sum s), so a chunk's effect on the state is its end state from zero and the sum
@@ -26,7 +26,7 @@ namespace sdm {
 namespace ssm {
 
 constexpr int SCAN_TILE = 16;   // tokens staged and walked at a time
-constexpr int SCAN_STAGES = 4;  // tiles in shared memory: one in use, three on their way
+constexpr int SCAN_STAGES = 6;  // tiles in shared memory: three in use, three on their way
 constexpr int SCAN_GRP = 8;     // tokens whose outputs are summed over a channel's lanes together
 enum { SCAN_OUT = 0, SCAN_CHUNK = 1, SCAN_CHUNK_REV = 2 };  // what a walk computes
 
@@ -120,11 +120,11 @@ struct RowCopy {
         if (piece >= PIECE) {
             const int lane = threadIdx.x & 31;
             const uint32_t dst = (uint32_t)__cvta_generic_to_shared(s) + lane * PIECE;
+            if (TILE * PER >= 32 || lane < TILE * PER) {
 #pragma unroll
-            for (int i = 0; i < ITER; ++i) {
-                if (TILE * PER < 32 && lane >= TILE * PER) break;
-                copy<PIECE>(dst + i * 32 * PIECE, next + i * RSTEP * stride * (long long)sizeof(T),
-                            lane / PER + i * RSTEP < left ? bytes : 0);
+                for (int i = 0; i < ITER; ++i)
+                    copy<PIECE>(dst + i * 32 * PIECE, next + i * RSTEP * stride * (long long)sizeof(T),
+                                lane / PER + i * RSTEP < left ? bytes : 0);
             }
             next += TILE * stride * (long long)sizeof(T);
         } else if (piece == 8) {
@@ -147,19 +147,32 @@ SDM_DEV void async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Rows of float as they are, rows of bf16 converted to floats in `f`; by the warp.
-template <typename T, int COUNT>
-SDM_DEV const float* rows_as_float(const T* s, float* f) {
-    if constexpr (sizeof(T) == 4) {
-        return reinterpret_cast<const float*>(s);
-    } else {
+// N consecutive floats from shared memory.
+template <int N>
+SDM_DEV void row_floats(const float* p, float (&v)[N]) {
 #pragma unroll
-        for (int i = (threadIdx.x & 31) * 4; i < COUNT; i += 128) {
-            float v[4];
-            Vec<4>::load(s + i, v);
-            Vec<4>::store(f + i, v);
+    for (int i = 0; i < N; i += 4) {
+        const float4 x = *reinterpret_cast<const float4*>(p + i);
+        v[i] = x.x, v[i + 1] = x.y, v[i + 2] = x.z, v[i + 3] = x.w;
+    }
+}
+
+// Sum of a channel's LN neighbouring shares.
+template <int LN>
+SDM_DEV float share_sum(const float* p) {
+    if constexpr (LN == 1) {
+        return p[0];
+    } else if constexpr (LN == 2) {
+        const float2 v = *reinterpret_cast<const float2*>(p);
+        return v.x + v.y;
+    } else {
+        float s = 0.f;
+#pragma unroll
+        for (int l = 0; l < LN; l += 4) {
+            const float4 v = *reinterpret_cast<const float4*>(p + l);
+            s += (v.x + v.y) + (v.z + v.w);
         }
-        return f;
+        return s;
     }
 }
 
@@ -225,10 +238,11 @@ struct ScanStage {
 };
 template <typename T, int NN, int WCH, int MODE>
 struct ScanShared {
+    static constexpr int WIDE = sizeof(T) == 2 ? SCAN_TILE * NN : 4;
     ScanStage<T, NN, WCH, MODE> st[SCAN_STAGES];
-    float B[SCAN_TILE * NN], C[SCAN_TILE * NN];  // the tile's, of bf16 rows
-    ulonglong2 tok[SCAN_TILE * WCH];             // a token's step twice, its step * u twice
-    f32x2 g[MODE == SCAN_CHUNK_REV ? SCAN_TILE * WCH : 2];  // its gated dy twice
+    float B[WIDE], C[MODE == SCAN_CHUNK ? 4 : WIDE];        // the tile's rows, of bf16
+    float2 tok[SCAN_TILE * WCH];                           // a token's step and step * u
+    float g[MODE == SCAN_CHUNK_REV ? SCAN_TILE * WCH : 4];  // its gated dy
     float y[MODE == SCAN_OUT ? SCAN_TILE * 32 : 4];         // each lane's share of its sum C h
 };
 
@@ -236,12 +250,21 @@ struct ScanShared {
 // sequence ends in it).  SCAN_CHUNK: its end state from zero and the sum of its steps;
 // SCAN_CHUNK_REV: also what its outputs' gradients carry to the token before it,
 // sum_t (prod_{s<=t} a_s) C_t dy_t.
+//
+// Three things overlap in an iteration, so that the few warps that there are keep the units busy:
+// the walk of tile i, the steps of tile i+1 (with its rows of B and C as floats) and the outputs of
+// tile i-1.  What they read from shared memory is loaded first, what they write is stored last, and
+// nothing in between branches (the flags are masks, the tiles before the first and behind the last
+// are computed from what lies there and dropped), so the compiler mixes their arithmetic.
+// Shared memory gives the registers 128 bytes a clock, broadcast or not, which is why a token's
+// step and input are two words and not two pairs.  Registers: 168 let three warps live on a
+// sub-partition; two of eight states a lane do better with more.
 template <typename T, int NPT, int LN, int MODE>
-__global__ void __launch_bounds__(32) scan_walk_kernel(ScanArgs<T> a) {
+__global__ void __launch_bounds__(32, NPT <= 4 ? 12 : 8) scan_walk_kernel(ScanArgs<T> a) {
     constexpr int NN = NPT * LN, NP = NPT / 2, WCH = 32 / LN;
     constexpr int PAIRS = SCAN_TILE * WCH / 64;  // of (token, channel pair) a lane
     constexpr int SB = NP >= 8 ? 2 : (NP >= 4 ? 4 : 8);  // tokens whose decays are computed ahead
-    constexpr bool OUT = MODE == SCAN_OUT, REV = MODE == SCAN_CHUNK_REV;
+    constexpr bool OUT = MODE == SCAN_OUT, REV = MODE == SCAN_CHUNK_REV, WIDE = sizeof(T) == 2;
     extern __shared__ __align__(16) char smem[];
     using Shared = ScanShared<T, NN, WCH, MODE>;
     Shared& sh = *reinterpret_cast<Shared*>(smem);
@@ -275,23 +298,24 @@ __global__ void __launch_bounds__(32) scan_walk_kernel(ScanArgs<T> a) {
 #pragma unroll 1
     for (int i = 0; i < SCAN_STAGES - 1; ++i) fetch(i);
 
-    float tmp[NPT];
-    f32x2 A2[NP], h[NP], r[NP], P[NP];
-    L.load(a.A + (long long)L.c * a.N, a.N, tmp);
+    float tmp[NPT], A2[NPT];
+    f32x2 h[NP], r[NP], P[NP];
+    L.load(a.A + (long long)L.c * a.N, a.N, A2);
 #pragma unroll
-    for (int i = 0; i < NP; ++i) {
-        A2[i] = pack2(tmp[2 * i] * kLog2e, tmp[2 * i + 1] * kLog2e);
-        r[i] = dup2(0.f);
-        P[i] = dup2(1.f);
+    for (int i = 0; i < NPT; ++i) {
+        A2[i] *= kLog2e;
+        tmp[i] = 0.f;
     }
-#pragma unroll
-    for (int i = 0; i < NPT; ++i) tmp[i] = 0.f;
     const long long at = ((long long)L.b * a.nchunk + blockIdx.y) * a.D + L.c;
     float* state = OUT && a.state ? a.state + ((long long)L.b * a.D + L.c) * a.N : nullptr;
     if (OUT && a.nchunk > 1) L.load(a.E + at * a.N, a.N, tmp);
     else if (state && !a.fresh) L.load(state, a.N, tmp);
 #pragma unroll
-    for (int i = 0; i < NP; ++i) h[i] = pack2(tmp[2 * i], tmp[2 * i + 1]);
+    for (int i = 0; i < NP; ++i) {
+        h[i] = pack2(tmp[2 * i], tmp[2 * i + 1]);
+        r[i] = dup2(0.f);
+        P[i] = dup2(1.f);
+    }
 
     // before and after the walk a lane looks after two channels, of every (64/WCH)-th token
     const int ic = 2 * (lane % (WCH / 2));
@@ -301,128 +325,180 @@ __global__ void __launch_bounds__(32) scan_walk_kernel(ScanArgs<T> a) {
     T* yp = OUT ? a.y.p + L.b * a.y.sb + L.c0 + ic : nullptr;
     const bool pair = OUT && ic + 1 < L.cols && ((uintptr_t)yp % (2 * sizeof(T))) == 0 && a.y.st % 2 == 0;
     f32x2 steps = dup2(0.f);
-    const ulonglong2* tok = sh.tok + lane / LN;
+    const unsigned long long m_sp = a.softplus ? ~0ull : 0ull, m_z = gate ? ~0ull : 0ull;
+    const float2* tok = sh.tok + lane / LN;
 
-    for (int tile = 0; t0 + tile * SCAN_TILE < t1; ++tile) {
-        const int tt = t0 + tile * SCAN_TILE;
-        async_wait<SCAN_STAGES - 2>();
-        __syncwarp();
-        fetch(tile + SCAN_STAGES - 1);  // into the stage that the tile before this one used
+    // the steps of a tile: its rows, then its words for the walk
+    f32x2 st2[PAIRS], su2[PAIRS], g2[PAIRS];
+    auto tile_steps = [&](int tile) {
         const auto& s = sh.st[tile % SCAN_STAGES];
 #pragma unroll
         for (int k = 0; k < PAIRS; ++k) {
             const int e = 2 * (lane + 32 * k);
-            float d[2], u[2];
+            float d[2], u[2], g[2], z[2];
             Vec<2>::load(s.d + e, d);
             Vec<2>::load(s.u + e, u);
-            f32x2 st2 = add2(pack2(d[0], d[1]), bias);
-            if (a.softplus) st2 = softplus2(st2);
-            if (tt + e / WCH >= t1) st2 = dup2(0.f);  // behind the sequence: the state stays
-            const f32x2 su2 = mul2(st2, pack2(u[0], u[1]));
-            float s0, s1, w0, w1;
-            unpack2(st2, s0, s1);
-            unpack2(su2, w0, w1);
-            sh.tok[e] = make_ulonglong2(dup2(s0), dup2(w0));
-            sh.tok[e + 1] = make_ulonglong2(dup2(s1), dup2(w1));
-            if (!OUT) steps = add2(steps, st2);
+            if (REV) Vec<2>::load(s.dy + e, g);
+            if (REV) Vec<2>::load(s.z + e, z);
+            st2[k] = add2(pack2(d[0], d[1]), bias);
+            const f32x2 sp = softplus2(st2[k]);
+            st2[k] = (sp & m_sp) | (st2[k] & ~m_sp);
+            st2[k] &= t0 + tile * SCAN_TILE + e / WCH < t1 ? ~0ull : 0ull;  // else the state stays
+            su2[k] = mul2(st2[k], pack2(u[0], u[1]));
+            if (!OUT) steps = add2(steps, st2[k]);
             if (REV) {
-                float g[2];
-                Vec<2>::load(s.dy + e, g);
-                f32x2 g2 = pack2(g[0], g[1]);
-                if (gate) {
-                    float z[2];
-                    Vec<2>::load(s.z + e, z);
-                    g2 = mul2(g2, silu2(pack2(z[0], z[1])));
-                }
-                unpack2(g2, g[0], g[1]);
-                sh.g[e] = dup2(g[0]);
-                sh.g[e + 1] = dup2(g[1]);
+                g2[k] = pack2(g[0], g[1]);
+                const f32x2 gz = mul2(g2[k], silu2(pack2(z[0], z[1])));
+                g2[k] = (gz & m_z) | (g2[k] & ~m_z);
             }
         }
-        const float* Bs = rows_as_float<T, SCAN_TILE * NN>(s.B, sh.B) + L.n0;
-        const float* Cs = nullptr;
-        if (OUT || REV) Cs = rows_as_float<T, SCAN_TILE * NN>(s.C, sh.C) + L.n0;
+    };
+    auto put_steps = [&]() {
+#pragma unroll
+        for (int k = 0; k < PAIRS; ++k) {
+            const int e = 2 * (lane + 32 * k);
+            float s0, s1, w0, w1;
+            unpack2(st2[k], s0, s1);
+            unpack2(su2[k], w0, w1);
+            *reinterpret_cast<float4*>(sh.tok + e) = make_float4(s0, w0, s1, w1);
+            if (REV) *reinterpret_cast<f32x2*>(sh.g + e) = g2[k];
+        }
+    };
+    // the outputs of a tile whose sums are in sh.y
+    f32x2 o2[PAIRS];
+    auto tile_outputs = [&](int tile) {
+        const auto& s = sh.st[tile % SCAN_STAGES];
+#pragma unroll
+        for (int k = 0; k < PAIRS; ++k) {
+            const int e = 2 * (lane + 32 * k);
+            float u[2], z[2];
+            const f32x2 y = pack2(share_sum<LN>(sh.y + e * LN), share_sum<LN>(sh.y + (e + 1) * LN));
+            Vec<2>::load(s.u + e, u);
+            Vec<2>::load(s.z + e, z);
+            o2[k] = fma2(skip, pack2(u[0], u[1]), y);
+            const f32x2 oz = mul2(o2[k], silu2(pack2(z[0], z[1])));
+            o2[k] = (oz & m_z) | (o2[k] & ~m_z);
+        }
+    };
+    auto put_outputs = [&](int tile) {
+#pragma unroll
+        for (int k = 0; k < PAIRS; ++k) {
+            const int t = t0 + tile * SCAN_TILE + 2 * (lane + 32 * k) / WCH;
+            if (t >= t0 && t < t1) {
+                float y[2];
+                unpack2(o2[k], y[0], y[1]);
+                T* o = yp + t * a.y.st;
+                if (pair) {
+                    Vec<2>::store(o, y);
+                } else {
+                    if (ic < L.cols) st(o, y[0]);
+                    if (ic + 1 < L.cols) st(o + 1, y[1]);
+                }
+            }
+        }
+    };
+
+    // a tile's rows of B and C, of bf16, as floats
+    constexpr int RW = WIDE ? (SCAN_TILE * NN + 255) / 256 : 0;
+    float wB[RW + 1][8], wC[RW + 1][8];
+    auto wide_rows = [&](int tile) {
+        if constexpr (WIDE) {
+            const auto& s = sh.st[tile % SCAN_STAGES];
+#pragma unroll
+            for (int k = 0; k < RW; ++k) {
+                const int e = (lane + 32 * k) * 8 % (SCAN_TILE * NN);  // a small tile: some twice
+                Vec<8>::load(s.B + e, wB[k]);
+                if (OUT || REV) Vec<8>::load(s.C + e, wC[k]);
+            }
+        }
+    };
+    auto put_rows = [&]() {
+#pragma unroll
+        for (int k = 0; k < RW; ++k) {
+            const int e = (lane + 32 * k) * 8 % (SCAN_TILE * NN);
+#pragma unroll
+            for (int i = 0; i < 8; i += 4) {
+                *reinterpret_cast<float4*>(sh.B + e + i) =
+                    make_float4(wB[k][i], wB[k][i + 1], wB[k][i + 2], wB[k][i + 3]);
+                if (OUT || REV)
+                    *reinterpret_cast<float4*>(sh.C + e + i) =
+                        make_float4(wC[k][i], wC[k][i + 1], wC[k][i + 2], wC[k][i + 3]);
+            }
+        }
+    };
+
+    const int tiles = max(0, (t1 - t0 + SCAN_TILE - 1) / SCAN_TILE);
+    if (tiles > 0) {
+        async_wait<SCAN_STAGES - 2>();
         __syncwarp();
-        float ysh[OUT ? SCAN_TILE : 1];  // stored behind the walk: its loads can be moved up
+        tile_steps(0);
+        wide_rows(0);
+        put_steps();
+        put_rows();
+        async_wait<SCAN_STAGES - 3>();
+        __syncwarp();
+    }
+    for (int tile = 0; tile < tiles; ++tile) {
+        if (OUT) tile_outputs(tile + SCAN_STAGES - 1);  // of the tile before this one
+        tile_steps(tile + 1);
+        wide_rows(tile + 1);
+        const float* Bs = (WIDE ? sh.B : reinterpret_cast<const float*>(sh.st[tile % SCAN_STAGES].B)) + L.n0;
+        const float* Cs = (WIDE ? sh.C : reinterpret_cast<const float*>(sh.st[tile % SCAN_STAGES].C)) + L.n0;
+        float y[SCAN_TILE];
 #pragma unroll
         for (int q0 = 0; q0 < SCAN_TILE; q0 += SB) {
             f32x2 dec[SB][NP], in[SB][NP];
 #pragma unroll
             for (int i = 0; i < SB; ++i) {
-                const ulonglong2 x = tok[(q0 + i) * WCH];
-                const f32x2* Br = reinterpret_cast<const f32x2*>(Bs + (q0 + i) * NN);
+                const float2 x = tok[(q0 + i) * WCH];
+                float B[NPT];
+                row_floats<NPT>(Bs + (q0 + i) * NN, B);
 #pragma unroll
                 for (int p = 0; p < NP; ++p) {
-                    dec[i][p] = exp2_pair(mul2(x.x, A2[p]));
-                    in[i][p] = mul2(x.y, Br[p]);
+                    dec[i][p] = pack2(exp2_fast(x.x * A2[2 * p]), exp2_fast(x.x * A2[2 * p + 1]));
+                    in[i][p] = pack2(x.y * B[2 * p], x.y * B[2 * p + 1]);
                 }
             }
 #pragma unroll
             for (int i = 0; i < SB; ++i) {
-                const f32x2* Cr = reinterpret_cast<const f32x2*>(Cs + (q0 + i) * NN);
-                f32x2 acc = dup2(0.f), g2;
-                if (REV) g2 = sh.g[(q0 + i) * WCH + lane / LN];
+                float C[NPT], g = 0.f;
+                if (OUT || REV) row_floats<NPT>(Cs + (q0 + i) * NN, C);
+                if (REV) g = sh.g[(q0 + i) * WCH + lane / LN];
+                f32x2 acc = dup2(0.f);
 #pragma unroll
                 for (int p = 0; p < NP; ++p) {
                     h[p] = fma2(dec[i][p], h[p], in[i][p]);
-                    if (OUT) acc = p == 0 ? mul2(h[p], Cr[p]) : fma2(h[p], Cr[p], acc);
+                    if (OUT) {
+                        const f32x2 c2 = pack2(C[2 * p], C[2 * p + 1]);
+                        acc = p == 0 ? mul2(h[p], c2) : fma2(h[p], c2, acc);
+                    }
                     if (REV) {
                         P[p] = mul2(P[p], dec[i][p]);
-                        r[p] = fma2(P[p], mul2(g2, Cr[p]), r[p]);
+                        r[p] = fma2(P[p], pack2(g * C[2 * p], g * C[2 * p + 1]), r[p]);
                     }
                 }
                 if (OUT) {
                     float lo, hi;
                     unpack2(acc, lo, hi);
-                    ysh[q0 + i] = lo + hi;
+                    y[q0 + i] = lo + hi;
                 }
             }
         }
+        __syncwarp();  // the tile's words and the outputs' stage have been read
         if (OUT) {
 #pragma unroll
-            for (int q = 0; q < SCAN_TILE; ++q) sh.y[q * 32 + lane] = ysh[q];
+            for (int q = 0; q < SCAN_TILE; ++q) sh.y[q * 32 + lane] = y[q];
+            put_outputs(tile - 1);
         }
+        put_steps();
+        put_rows();
+        fetch(tile + SCAN_STAGES - 1);  // into the stage of the tile before this one
+        async_wait<SCAN_STAGES - 3>();  // the tile after the next is there
         __syncwarp();
-        if (OUT) {
-#pragma unroll
-            for (int k = 0; k < PAIRS; ++k) {
-                const int e = 2 * (lane + 32 * k), t = tt + e / WCH;
-                float y[2], u[2];
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {  // the shares of the channel's lanes
-                    const float* sy = sh.y + (e + j) * LN;
-                    if (LN == 1) {
-                        y[j] = sy[0];
-                    } else if (LN == 2) {
-                        y[j] = sy[0] + sy[1];
-                    } else {
-                        y[j] = 0.f;
-#pragma unroll
-                        for (int l = 0; l < LN; l += 4) {
-                            const float4 v = *reinterpret_cast<const float4*>(sy + l);
-                            y[j] += (v.x + v.y) + (v.z + v.w);
-                        }
-                    }
-                }
-                Vec<2>::load(s.u + e, u);
-                f32x2 v = fma2(skip, pack2(u[0], u[1]), pack2(y[0], y[1]));
-                if (gate) {
-                    float z[2];
-                    Vec<2>::load(s.z + e, z);
-                    v = mul2(v, silu2(pack2(z[0], z[1])));
-                }
-                unpack2(v, y[0], y[1]);
-                if (t < t1) {
-                    T* o = yp + t * a.y.st;
-                    if (pair) {
-                        Vec<2>::store(o, y);
-                    } else {
-                        if (ic < L.cols) st(o, y[0]);
-                        if (ic + 1 < L.cols) st(o + 1, y[1]);
-                    }
-                }
-            }
-        }
+    }
+    if (OUT && tiles > 0) {
+        tile_outputs(tiles - 1);
+        put_outputs(tiles - 1);
     }
     if (OUT) {
         if (state && t1 == len) {

@@ -217,20 +217,21 @@ long long scan_warps(const sdm_scan_dims* d, int LN) {
     return (long long)d->B * d->G * ceil_div(d->D / d->G, 32 / LN);
 }
 
-// Lanes of a channel: as few as give every SM sub-partition two warps (fewer lanes share less
-// work, more lanes make more warps); then chunks of the tokens while some sub-partitions would
-// idle, since a second pass over the exponentials costs more than it gains above that.
+// Eight states a lane where that makes five warps an SM, else four.  (16 states, bf16, 1024 tokens
+// of 4096 channels: 2 sequences take 95 us in 512 warps of eight a lane and 91 us in 1024 of four,
+// 4 sequences 133 and 177 us; sixteen a lane in one warp of 32 channels 216 us.)  Then chunks of the
+// tokens while half of the SMs' sub-partitions would have no warp: a second pass over the
+// exponentials costs more than it gains above that (at 512 warps 77 us against 70 us).
 ScanPlan scan_plan(const sdm_scan_dims* d) {
     ScanPlan p{};
     p.NN = pad_states(d->N);
-    const int lo = p.NN <= 16 ? 1 : p.NN / 16, hi = p.NN == 8 ? 4 : 8;
-    p.LN = lo;
-    while (p.LN < hi && scan_warps(d, p.LN) < 8 * kSms) p.LN *= 2;
+    p.LN = p.NN / 8;
+    if (p.LN < 8 && scan_warps(d, p.LN) < 5 * kSms) p.LN *= 2;
     const long long warps = scan_warps(d, p.LN);
     p.chunk = std::max(1, d->T);
     p.nchunk = 1;
     if (warps <= 2 * kSms) {
-        const long long want = std::min(ceil_div(d->T, 64), 16 * kSms / warps);
+        const long long want = std::min(ceil_div(d->T, 64), 8 * kSms / warps);
         if (want > 1) {
             p.chunk = (int)(ceil_div(ceil_div(d->T, want), SCAN_TILE) * SCAN_TILE);
             p.nchunk = (int)ceil_div(d->T, p.chunk);
@@ -330,19 +331,18 @@ sdm_status run_scan(const sdm_scan_dims* d, ScanArgs<T> a, const sdm_view* const
     a.chunk = p.chunk, a.nchunk = p.nchunk;
     a.E = static_cast<float*>(ws);
     a.S = reinterpret_cast<float*>(static_cast<char*>(ws) + p.off_S);
-    switch (p.NN * 16 + p.LN) {
-        case 8 * 16 + 1: return launch_scan_t<T, 8, 1>(a, v, s);
-        case 8 * 16 + 2: return launch_scan_t<T, 4, 2>(a, v, s);
-        case 8 * 16 + 4: return launch_scan_t<T, 2, 4>(a, v, s);
-        case 16 * 16 + 1: return launch_scan_t<T, 16, 1>(a, v, s);
-        case 16 * 16 + 2: return launch_scan_t<T, 8, 2>(a, v, s);
-        case 16 * 16 + 4: return launch_scan_t<T, 4, 4>(a, v, s);
-        case 16 * 16 + 8: return launch_scan_t<T, 2, 8>(a, v, s);
-        case 32 * 16 + 2: return launch_scan_t<T, 16, 2>(a, v, s);
-        case 32 * 16 + 4: return launch_scan_t<T, 8, 4>(a, v, s);
-        case 32 * 16 + 8: return launch_scan_t<T, 4, 8>(a, v, s);
-        case 64 * 16 + 4: return launch_scan_t<T, 16, 4>(a, v, s);
-        default: return launch_scan_t<T, 8, 8>(a, v, s);
+    if (p.LN * 8 == p.NN) {
+        switch (p.LN) {
+            case 1: return launch_scan_t<T, 8, 1>(a, v, s);
+            case 2: return launch_scan_t<T, 8, 2>(a, v, s);
+            case 4: return launch_scan_t<T, 8, 4>(a, v, s);
+            default: return launch_scan_t<T, 8, 8>(a, v, s);
+        }
+    }
+    switch (p.LN) {
+        case 2: return launch_scan_t<T, 4, 2>(a, v, s);
+        case 4: return launch_scan_t<T, 4, 4>(a, v, s);
+        default: return launch_scan_t<T, 4, 8>(a, v, s);
     }
 }
 

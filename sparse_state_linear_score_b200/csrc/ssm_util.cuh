@@ -70,6 +70,15 @@ struct Vec<4> {
 };
 
 template <>
+struct Vec<8> {  // bf16 only: 16 bytes
+    SDM_DEV static void load(const bf16* p, float (&v)[8]) {
+        const uint4 x = *reinterpret_cast<const uint4*>(p);
+        v[0] = bf16_lo(x.x), v[1] = bf16_hi(x.x), v[2] = bf16_lo(x.y), v[3] = bf16_hi(x.y);
+        v[4] = bf16_lo(x.z), v[5] = bf16_hi(x.z), v[6] = bf16_lo(x.w), v[7] = bf16_hi(x.w);
+    }
+};
+
+template <>
 struct Vec<2> {
     SDM_DEV static void load(const float* p, float (&v)[2]) {
         const float2 x = *reinterpret_cast<const float2*>(p);
