@@ -37,26 +37,106 @@ struct ConvArgs {
     int run, runs;  // tokens of a run, runs of a sequence
 };
 
+template <bool B>
+struct Flag {
+    static constexpr bool value = B;
+};
+
+// V channels of a token as they are stored: what a load in flight leaves in registers, so that
+// nothing waits for it before its values are used.
+template <typename T, int V>
+struct Raw;
+template <>
+struct Raw<float, 4> {
+    float4 x;
+    SDM_DEV void clear() { x = make_float4(0.f, 0.f, 0.f, 0.f); }
+    SDM_DEV void load(const float* p) { x = *reinterpret_cast<const float4*>(p); }
+    SDM_DEV void pairs(f32x2 (&v)[2]) const { v[0] = pack2(x.x, x.y), v[1] = pack2(x.z, x.w); }
+};
+template <>
+struct Raw<bf16, 4> {
+    uint2 x;
+    SDM_DEV void clear() { x = make_uint2(0u, 0u); }
+    SDM_DEV void load(const bf16* p) { x = *reinterpret_cast<const uint2*>(p); }
+    SDM_DEV void pairs(f32x2 (&v)[2]) const {
+        v[0] = pack2(bf16_lo(x.x), bf16_hi(x.x)), v[1] = pack2(bf16_lo(x.y), bf16_hi(x.y));
+    }
+};
+template <typename T>
+struct Raw<T, 1> {
+    T x;
+    SDM_DEV void clear() { x = T(0.f); }
+    SDM_DEV void load(const T* p) { x = *p; }
+    SDM_DEV void pairs(f32x2 (&v)[1]) const { v[0] = pack2(ld(&x), 0.f); }
+};
+
+// The same as pairs of floats (one channel: a pair with a zero).
+template <int V>
+struct Pairs {
+    static constexpr int N = (V + 1) / 2;
+    template <typename T>
+    SDM_DEV static void load(const T* p, f32x2 (&v)[N]) {
+        float x[V];
+        Vec<V>::load(p, x);
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = pack2(x[2 * i], 2 * i + 1 < V ? x[2 * i + 1 < V ? 2 * i + 1 : 0] : 0.f);
+    }
+    template <typename T>
+    SDM_DEV static void store(T* p, const f32x2 (&v)[N]) {
+        float x[2 * N], y[V];
+#pragma unroll
+        for (int i = 0; i < N; ++i) unpack2(v[i], x[2 * i], x[2 * i + 1]);
+#pragma unroll
+        for (int i = 0; i < V; ++i) y[i] = x[i];
+        Vec<V>::store(p, y);
+    }
+};
+
+// The filters w[j] and biases of channels ch .. ch+V-1.
+template <int V, int K>
+SDM_DEV void conv_load_filter(const float* w, const float* bias, long long ch,
+                              f32x2 (&wr)[K][Pairs<V>::N], f32x2 (&br)[Pairs<V>::N]) {
+    float x[V * K];
+    if constexpr (V == 4) {  // V*K floats from a multiple of 16 bytes
+#pragma unroll
+        for (int i = 0; i < V * K; i += 4) {
+            const float4 q = *reinterpret_cast<const float4*>(w + ch * K + i);
+            x[i] = q.x, x[i + 1] = q.y, x[i + 2] = q.z, x[i + 3] = q.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V * K; ++i) x[i] = w[ch * K + i];
+    }
+#pragma unroll
+    for (int p = 0; p < Pairs<V>::N; ++p) {
+#pragma unroll
+        for (int j = 0; j < K; ++j)
+            wr[j][p] = pack2(x[2 * p * K + j], 2 * p + 1 < V ? x[(2 * p + 1) % V * K + j] : 0.f);
+        br[p] = dup2(0.f);
+    }
+    if (bias) Pairs<V>::load(bias + ch, br);
+}
+
 // Tokens t0-K+1 .. t0-1 of the sequence: from x, or before its start from the state.
 template <typename T, int V, int K>
 SDM_DEV void conv_load_window(const ConvArgs<T>& a, const T* x, const T* state, int t0, int len,
-                              float (&win)[K][V]) {
+                              f32x2 (&win)[K][Pairs<V>::N]) {
 #pragma unroll
     for (int j = 0; j < K - 1; ++j) {
         const int s = t0 - (K - 1) + j;
 #pragma unroll
-        for (int v = 0; v < V; ++v) win[j][v] = 0.f;
+        for (int p = 0; p < Pairs<V>::N; ++p) win[j][p] = dup2(0.f);
         if (s >= 0) {
-            if (s < len) Vec<V>::load(x + s * a.x.st, win[j]);
+            if (s < len) Pairs<V>::load(x + s * a.x.st, win[j]);
         } else if (state) {
-            Vec<V>::load(state + (long long)(s + K - 1) * a.d, win[j]);
+            Pairs<V>::load(state + (long long)(s + K - 1) * a.d, win[j]);
         }
     }
 }
 
 template <typename T, int V, int K>
 __global__ void __launch_bounds__(CONV_WARPS * 32) short_conv_kernel(ConvArgs<T> a) {
-    constexpr int U = K <= 4 ? 8 : 4;  // tokens whose loads are in flight together
+    constexpr int U = 8, N = Pairs<V>::N;  // U tokens' loads are in flight together
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int nv = a.d / V;
     const long long cv = (long long)blockIdx.x * 32 + lane;
@@ -64,7 +144,6 @@ __global__ void __launch_bounds__(CONV_WARPS * 32) short_conv_kernel(ConvArgs<T>
     if (cv >= (long long)a.H * nv || rr >= (long long)a.B * a.runs) return;
     const int h = (int)(cv / nv), c = (int)(cv % nv) * V;
     const int b = (int)(rr / a.runs), run = (int)(rr % a.runs);
-    const long long ch = (long long)h * a.d + c;
     const int len = clamp_len(a.lens, b, a.T_);
     const int t0 = run * a.run;
     if (t0 >= len && run > 0) return;
@@ -73,58 +152,55 @@ __global__ void __launch_bounds__(CONV_WARPS * 32) short_conv_kernel(ConvArgs<T>
     T* y = a.y.p + b * a.y.sb + h * a.y.sh + c;
     T* state = a.state ? a.state + ((long long)b * a.H + h) * (K - 1) * a.d + c : nullptr;
 
-    float w[K][V], bias[V], win[K][V];
+    Raw<T, V> in[U];
+    auto fetch = [&](int t) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
+        for (int i = 0; i < U; ++i)
+            if (t + i < t1) in[i].load(x + (t + i) * a.x.st);
+    };
 #pragma unroll
-        for (int j = 0; j < K; ++j) w[j][v] = a.w[(ch + v) * K + j];
-        bias[v] = a.bias ? a.bias[ch + v] : 0.f;
-    }
+    for (int i = 0; i < U; ++i) in[i].clear();
+    fetch(t0);
+    f32x2 w[K][N], bias[N], win[K][N];
+    conv_load_filter<V, K>(a.w, a.bias, (long long)h * a.d + c, w, bias);
     conv_load_window<T, V, K>(a, x, a.fresh ? nullptr : state, t0, len, win);
 
     // The sequence's first run also moves the state on: the K-1 inputs that end at len, from x
-    // or, where the call is shorter, from the old state (which is in the window).
+    // or, where the call is shorter, from later rows of the old state, all read before any is
+    // written.
     if (run == 0 && state) {
-        float keep[K][V];
+        f32x2 keep[K][N];
 #pragma unroll
         for (int k = 0; k < K - 1; ++k) {
             const int s = len - (K - 1) + k;
-            if (s >= 0) {
-                Vec<V>::load(x + s * a.x.st, keep[k]);
-            } else {
 #pragma unroll
-                for (int q = 0; q < K - 1; ++q)
-                    if (q == s + K - 1) {
-#pragma unroll
-                        for (int v = 0; v < V; ++v) keep[k][v] = win[q][v];
-                    }
-            }
+            for (int p = 0; p < N; ++p) keep[k][p] = dup2(0.f);
+            if (s >= 0) Pairs<V>::load(x + s * a.x.st, keep[k]);
+            else if (!a.fresh) Pairs<V>::load(state + (long long)(len + k) * a.d, keep[k]);
         }
 #pragma unroll
-        for (int k = 0; k < K - 1; ++k) Vec<V>::store(state + (long long)k * a.d, keep[k]);
+        for (int k = 0; k < K - 1; ++k) Pairs<V>::store(state + (long long)k * a.d, keep[k]);
     }
 
     for (int t = t0; t < t1; t += U) {
-        float in[U][V];
+        f32x2 cur[U][N];
 #pragma unroll
-        for (int i = 0; i < U; ++i)
-            if (t + i < t1) Vec<V>::load(x + (t + i) * a.x.st, in[i]);
+        for (int i = 0; i < U; ++i) in[i].pairs(cur[i]);
+        fetch(t + U);
 #pragma unroll
         for (int i = 0; i < U; ++i) {
-            if (t + i < t1) {
-                float p[V];
+            f32x2 o[N];
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    win[K - 1][v] = in[i][v];
-                    p[v] = bias[v];
+            for (int p = 0; p < N; ++p) {
+                win[K - 1][p] = cur[i][p];
+                o[p] = bias[p];
 #pragma unroll
-                    for (int j = 0; j < K; ++j) p[v] = fmaf(w[j][v], win[j][v], p[v]);
+                for (int j = 0; j < K; ++j) o[p] = fma2(w[j][p], win[j][p], o[p]);
 #pragma unroll
-                    for (int j = 0; j < K - 1; ++j) win[j][v] = win[j + 1][v];
-                    if (a.act) p[v] *= sigmoid(p[v]);
-                }
-                Vec<V>::store(y + (t + i) * a.y.st, p);
+                for (int j = 0; j < K - 1; ++j) win[j][p] = win[j + 1][p];
+                if (a.act) o[p] = silu2(o[p]);
             }
+            if (t + i < t1) Pairs<V>::store(y + (t + i) * a.y.st, o);
         }
     }
 }
@@ -133,27 +209,23 @@ __global__ void __launch_bounds__(CONV_WARPS * 32) short_conv_kernel(ConvArgs<T>
 // registers; the block's warps are added in order in shared memory, the blocks in order by
 // conv_sum_kernel.
 template <typename T, int V, int K>
-__global__ void __launch_bounds__(CONV_WARPS * 32) short_conv_bwd_kernel(ConvArgs<T> a) {
-    constexpr int U = 4;
-    __shared__ float s_part[CONV_WARPS][K + 1][V][32];
+__global__ void __launch_bounds__(CONV_WARPS * 32, K <= 4 ? 3 : 1) short_conv_bwd_kernel(ConvArgs<T> a) {
+    constexpr int U = 4, N = Pairs<V>::N;
+    __shared__ float s_part[CONV_WARPS][K + 1][2 * N][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int nv = a.d / V;
     const long long C = (long long)a.H * a.d;
     const long long cv = (long long)blockIdx.x * 32 + lane;
     const bool live = cv < (long long)a.H * nv;
     const int h = live ? (int)(cv / nv) : 0, c = live ? (int)(cv % nv) * V : 0;
-    const long long ch = (long long)h * a.d + c;
 
-    float w[K][V], bias[V], dw[K][V], db[V];
+    f32x2 w[K][N], bias[N], dw[K][N], db[N];
+    conv_load_filter<V, K>(a.w, a.bias, (long long)h * a.d + c, w, bias);
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
+    for (int p = 0; p < N; ++p) {
 #pragma unroll
-        for (int j = 0; j < K; ++j) {
-            w[j][v] = a.w[(ch + v) * K + j];
-            dw[j][v] = 0.f;
-        }
-        bias[v] = a.bias ? a.bias[ch + v] : 0.f;
-        db[v] = 0.f;
+        for (int j = 0; j < K; ++j) dw[j][p] = dup2(0.f);
+        db[p] = dup2(0.f);
     }
     const long long nruns = live ? (long long)a.B * a.runs : 0;
     for (long long rr = (long long)blockIdx.y * CONV_WARPS + warp; rr < nruns;
@@ -166,80 +238,116 @@ __global__ void __launch_bounds__(CONV_WARPS * 32) short_conv_bwd_kernel(ConvArg
         T* dx = a.y.p + b * a.y.sb + h * a.y.sh + c;
         const long long so = ((long long)b * a.H + h) * (K - 1) * a.d + c;
         const T* state = a.state && !a.fresh ? a.state + so : nullptr;
-        float win[K][V], g[K][V];  // inputs and g of the last K tokens, oldest first
+        // Token t brings g_t and completes dx of token t-K+1; the run's last K-1 need the g of
+        // tokens behind it.  Inputs and g of the last K tokens, oldest first:
+        f32x2 win[K][N], g[K][N];
+        Raw<T, V> xi[U], gi[U];
+        const int tend = t1 + K - 1, tload = min(tend, len);
+        auto fetch = [&](int t) {
+            const T* xp = x + t * a.x.st;
+            const T* gp = dy + t * a.dy.st;
+            if (t + U <= tload) {
+#pragma unroll
+                for (int i = 0; i < U; ++i) {
+                    xi[i].load(xp + i * a.x.st);
+                    gi[i].load(gp + i * a.dy.st);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < U; ++i) {
+                    xi[i].clear();
+                    gi[i].clear();
+                    if (t + i < tload) {
+                        xi[i].load(xp + i * a.x.st);
+                        gi[i].load(gp + i * a.dy.st);
+                    }
+                }
+            }
+        };
+        // U tokens; EDGE: some of them, or the tokens they complete, lie outside the run, behind
+        // the sequence, before its start or in the state after the call.
+        auto group = [&](int t, auto edge) {
+            constexpr bool EDGE = decltype(edge)::value;
+            f32x2 cx[U][N], cg[U][N], out[U][N];
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                xi[i].pairs(cx[i]);
+                gi[i].pairs(cg[i]);
+            }
+            fetch(t + U);
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                const unsigned long long inside = !EDGE || t + i < len ? ~0ull : 0ull;
+                const unsigned long long own = !EDGE || t + i < t1 ? ~0ull : 0ull;
+#pragma unroll
+                for (int p = 0; p < N; ++p) {
+                    win[K - 1][p] = cx[i][p];
+                    f32x2 gt = cg[i][p];
+                    if (a.act) {
+                        f32x2 q = bias[p];
+#pragma unroll
+                        for (int j = 0; j < K; ++j) q = fma2(w[j][p], win[j][p], q);
+                        gt = mul2(gt, dsilu2(q));
+                    }
+                    if (EDGE) gt &= inside;  // also where q is not finite
+#pragma unroll
+                    for (int j = 0; j < K - 1; ++j) g[j][p] = g[j + 1][p];
+                    g[K - 1][p] = gt;
+                    if (EDGE) gt &= own;
+                    db[p] = add2(db[p], gt);
+#pragma unroll
+                    for (int j = 0; j < K; ++j) dw[j][p] = fma2(gt, win[j][p], dw[j][p]);
+                    out[i][p] = mul2(w[0][p], g[K - 1][p]);
+#pragma unroll
+                    for (int j = 1; j < K; ++j) out[i][p] = fma2(w[j][p], g[K - 1 - j][p], out[i][p]);
+#pragma unroll
+                    for (int j = 0; j < K - 1; ++j) win[j][p] = win[j + 1][p];
+                }
+            }
+            T* op = dx + (t - (K - 1)) * a.y.st;
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                if (!EDGE) {
+                    Pairs<V>::store(op + i * a.y.st, out[i]);
+                    continue;
+                }
+                const int s = t + i - (K - 1);
+                if (t + i >= tend || (s < t0 && run > 0)) continue;  // the run before has it
+                const int kept = s - len + K - 1;  // its row in the state after the call
+                if (a.dstate_end && kept >= 0 && kept < K - 1) {
+                    f32x2 e[N];
+                    Pairs<V>::load(a.dstate_end + so + (long long)kept * a.d, e);
+#pragma unroll
+                    for (int p = 0; p < N; ++p) out[i][p] = add2(out[i][p], e[p]);
+                }
+                if (s >= 0) Pairs<V>::store(dx + s * a.y.st, out[i]);
+                else if (a.dstate) Pairs<V>::store(a.dstate + so + (long long)(s + K - 1) * a.d, out[i]);
+            }
+        };
+        fetch(t0);
         conv_load_window<T, V, K>(a, x, state, t0, len, win);
 #pragma unroll
         for (int j = 0; j < K; ++j)
 #pragma unroll
-            for (int v = 0; v < V; ++v) g[j][v] = 0.f;
-        // Token t brings g_t and completes dx of token t-K+1; the run's last K-1 need the g of
-        // tokens behind it.
-        const int tend = t1 + K - 1, tload = min(tend, len);
+            for (int p = 0; p < N; ++p) g[j][p] = dup2(0.f);
+        const int inner = min(t1, len - (K - 1));  // tokens before it are in no state after the call
         for (int t = t0; t < tend; t += U) {
-            float xi[U][V], gi[U][V];
-#pragma unroll
-            for (int i = 0; i < U; ++i) {
-#pragma unroll
-                for (int v = 0; v < V; ++v) xi[i][v] = gi[i][v] = 0.f;
-                if (t + i < tload) {
-                    Vec<V>::load(x + (t + i) * a.x.st, xi[i]);
-                    Vec<V>::load(dy + (t + i) * a.dy.st, gi[i]);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < U; ++i) {
-                const int tt = t + i;
-                if (tt >= tend) break;
-                float out[V];
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    win[K - 1][v] = xi[i][v];
-                    float gt = gi[i][v];
-                    if (a.act) {
-                        float p = bias[v];
-#pragma unroll
-                        for (int j = 0; j < K; ++j) p = fmaf(w[j][v], win[j][v], p);
-                        const float sg = sigmoid(p);
-                        gt *= sg * (1.f + p * (1.f - sg));
-                    }
-                    if (tt >= len) gt = 0.f;  // also where p is not finite
-#pragma unroll
-                    for (int j = 0; j < K - 1; ++j) g[j][v] = g[j + 1][v];
-                    g[K - 1][v] = gt;
-                    if (tt < t1 && tt < len) {
-                        db[v] += gt;
-#pragma unroll
-                        for (int j = 0; j < K; ++j) dw[j][v] = fmaf(gt, win[j][v], dw[j][v]);
-                    }
-                    out[v] = 0.f;
-#pragma unroll
-                    for (int j = 0; j < K; ++j) out[v] = fmaf(w[j][v], g[K - 1 - j][v], out[v]);
-#pragma unroll
-                    for (int j = 0; j < K - 1; ++j) win[j][v] = win[j + 1][v];
-                }
-                const int s = tt - (K - 1);
-                if (s < t0 && run > 0) continue;  // the run before has it
-                const int kept = s - len + K - 1;  // its row in the state after the call
-                if (a.dstate_end && kept >= 0 && kept < K - 1) {
-                    float e[V];
-                    Vec<V>::load(a.dstate_end + so + (long long)kept * a.d, e);
-#pragma unroll
-                    for (int v = 0; v < V; ++v) out[v] += e[v];
-                }
-                if (s >= len && s >= 0) {
-#pragma unroll
-                    for (int v = 0; v < V; ++v) out[v] = 0.f;
-                }
-                if (s >= 0) Vec<V>::store(dx + s * a.y.st, out);
-                else if (a.dstate) Vec<V>::store(a.dstate + so + (long long)(s + K - 1) * a.d, out);
-            }
+            if (t >= t0 + K - 1 && t + U <= inner) group(t, Flag<false>());
+            else group(t, Flag<true>());
         }
     }
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
+    for (int p = 0; p < N; ++p) {
+        float lo, hi;
 #pragma unroll
-        for (int j = 0; j < K; ++j) s_part[warp][j][v][lane] = dw[j][v];
-        s_part[warp][K][v][lane] = db[v];
+        for (int j = 0; j < K; ++j) {
+            unpack2(dw[j][p], lo, hi);
+            s_part[warp][j][2 * p][lane] = lo;
+            s_part[warp][j][2 * p + 1][lane] = hi;
+        }
+        unpack2(db[p], lo, hi);
+        s_part[warp][K][2 * p][lane] = lo;
+        s_part[warp][K][2 * p + 1][lane] = hi;
     }
     __syncthreads();
     for (int e = threadIdx.x; e < (K + 1) * V * 32; e += CONV_WARPS * 32) {
@@ -253,18 +361,29 @@ __global__ void __launch_bounds__(CONV_WARPS * 32) short_conv_bwd_kernel(ConvArg
     }
 }
 
-// dw[c][j] and dbias[c] from the blocks' shares, in order.
-__global__ void __launch_bounds__(256) conv_sum_kernel(const float* part, int blocks, long long C,
-                                                       int K, float* dw, float* dbias) {
-    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
-    if (i >= C * (K + 1)) return;
+// dw[c][j] and dbias[c] from the blocks' shares, in order: eight interleaved segments of blocks, then
+// the segments.
+constexpr int CSUM_SEG = 8;
+__global__ void __launch_bounds__(32 * CSUM_SEG) conv_sum_kernel(const float* part, int blocks,
+                                                                 long long C, int K, float* dw,
+                                                                 float* dbias) {
+    __shared__ float s[CSUM_SEG][32];
+    const int lane = threadIdx.x & 31, seg = threadIdx.x >> 5;
+    const long long i = (long long)blockIdx.x * 32 + lane, n = C * (K + 1);
+    float sum = 0.f;
+    if (i < n) {
+#pragma unroll 4
+        for (int p = seg; p < blocks; p += CSUM_SEG) sum += part[p * n + i];
+    }
+    s[seg][lane] = sum;
+    __syncthreads();
+    if (seg > 0 || i >= n) return;
+#pragma unroll
+    for (int k = 1; k < CSUM_SEG; ++k) sum += s[k][lane];
     const long long c = i % C;
     const int j = (int)(i / C);
-    if (j == K && !dbias) return;
-    float sum = 0.f;
-    for (int p = 0; p < blocks; ++p) sum += part[((long long)p * (K + 1) + j) * C + c];
     if (j < K) dw[c * K + j] = sum;
-    else dbias[c] = sum;
+    else if (dbias) dbias[c] = sum;
 }
 
 }  // namespace ssm

@@ -108,16 +108,15 @@ ConvPlan conv_plan(const sdm_conv_dims* d, int V) {
     return p;
 }
 
-// The gradient's blocks along the runs: their shares of dw are added afterwards.
+// The gradient: three blocks an SM, all at once; their shares of dw are added afterwards.
 constexpr int kConvBwdRun = 64;
-constexpr int kConvBwdBlocks = 64;
 ConvPlan conv_bwd_plan(const sdm_conv_dims* d, int V) {
     ConvPlan p;
     p.gx = (unsigned)ceil_div((long long)d->H * (d->d / V), 32);
     p.run = kConvBwdRun;
     p.runs = (int)std::max(1LL, ceil_div(d->T, p.run));
-    const long long warps = (long long)d->B * p.runs;
-    p.gy = (unsigned)std::min<long long>(kConvBwdBlocks, ceil_div(warps, CONV_WARPS));
+    const long long need = ceil_div((long long)d->B * p.runs, CONV_WARPS);
+    p.gy = (unsigned)std::max(1LL, std::min(need, 3LL * kSms / p.gx));
     return p;
 }
 
@@ -188,8 +187,8 @@ sdm_status run_conv_bwd(const sdm_conv_dims* d, const sdm_view* x, const float* 
     const sdm_status e = launched();
     if (e) return e;
     const long long C = (long long)d->H * d->d;
-    conv_sum_kernel<<<(unsigned)ceil_div(C * (d->K + 1), 256), 256, 0, s>>>(a.part, (int)p.gy, C,
-                                                                           d->K, dw, dbias);
+    conv_sum_kernel<<<(unsigned)ceil_div(C * (d->K + 1), 32), 32 * CSUM_SEG, 0, s>>>(
+        a.part, (int)p.gy, C, d->K, dw, dbias);
     return launched();
 }
 
@@ -452,7 +451,6 @@ sdm_status check_scan_in(const sdm_scan_dims* d, const sdm_view* u, const sdm_vi
 
 // ---- block norms ---------------------------------------------------------------------------
 constexpr int kNormThreads = 512;
-constexpr int kNormBwdBlocks = 2 * kSms;
 
 sdm_status check_norm(const sdm_norm_dims* d) {
     if (!d) return SDM_ERR_ARG;
@@ -472,16 +470,28 @@ NormArgs norm_args(const sdm_norm_dims* d, const void* r, const void* f, const f
     return a;
 }
 
+// Threads of a block whose threads take P pieces of V values.
+unsigned norm_threads(int D, int V, int P) {
+    return (unsigned)(ceil_div(ceil_div(ceil_div(D, V), P), 32) * 32);
+}
+
+// Blocks: the forward pass two an SM (more where they are small), the gradient one of at most 512
+// threads, so that few shares of the sums are written.
+unsigned norm_blocks(const sdm_norm_dims* d, bool bwd) {
+    const int V = d->D % 4 == 0 ? 4 : 1;
+    const unsigned nt = norm_threads(d->D, V, V == 4 ? 2 : 8);
+    const long long per_sm = std::max<long long>(1, (bwd ? 512 : 1024) / nt);
+    return (unsigned)std::min<long long>(d->rows, kSms * std::min<long long>(per_sm, 16));
+}
+
 template <int V, int P>
 void launch_norm(const NormArgs& a, bool bwd, unsigned grid, cudaStream_t s) {
-    const long long nv = a.D / V;
-    const unsigned nt = (unsigned)(ceil_div(ceil_div(nv, P), 32) * 32);
+    const unsigned nt = norm_threads(a.D, V, P);
     if (bwd) block_norm_bwd_kernel<V, P><<<grid, nt, 0, s>>>(a);
     else block_norm_kernel<V, P><<<grid, nt, 0, s>>>(a);
 }
 
-// Values of a thread: few, so that the weights and a row fit its registers, in at most 512
-// threads.
+// Pieces of a thread: as few as fit a row into 512 threads.
 void launch_norm_any(const NormArgs& a, bool bwd, unsigned grid, cudaStream_t s) {
     if (a.D % 4 == 0) {
         if (a.D <= 2 * 4 * kNormThreads) return launch_norm<4, 2>(a, bwd, grid, s);
@@ -512,8 +522,9 @@ sdm_status sdm_short_conv(const sdm_conv_dims* dims, const sdm_view* x, const fl
 
 size_t sdm_short_conv_backward_workspace_bytes(const sdm_conv_dims* dims) {
     if (check_conv(dims) != SDM_OK) return 0;
-    const ConvPlan p = conv_bwd_plan(dims, 1);  // its second axis does not depend on the width
-    return up256((size_t)p.gy * (dims->K + 1) * dims->H * dims->d * 4);
+    const unsigned gy = std::max(conv_bwd_plan(dims, 1).gy,
+                                 dims->d % 4 == 0 ? conv_bwd_plan(dims, 4).gy : 0u);
+    return up256((size_t)gy * (dims->K + 1) * dims->H * dims->d * 4);
 }
 
 sdm_status sdm_short_conv_backward(const sdm_conv_dims* dims, const sdm_view* x, const float* w,
@@ -620,15 +631,13 @@ sdm_status sdm_block_norm(const sdm_norm_dims* dims, const void* r, const void* 
     if (dims->rows == 0) return SDM_OK;
     NormArgs a = norm_args(dims, r, f, w_post, gate, scale, w_pre);
     a.r_out = r_out, a.n = n;
-    const unsigned grid = (unsigned)std::min<long long>(dims->rows, kSms * 4);
-    launch_norm_any(a, false, grid, stream);
+    launch_norm_any(a, false, norm_blocks(dims, false), stream);
     return launched();
 }
 
 size_t sdm_block_norm_backward_workspace_bytes(const sdm_norm_dims* dims) {
     if (check_norm(dims) != SDM_OK) return 0;
-    const size_t blocks = (size_t)std::min<long long>(dims->rows, kNormBwdBlocks);
-    return up256(std::max<size_t>(1, blocks) * 3 * dims->D * 4);
+    return up256(std::max<size_t>(1, norm_blocks(dims, true)) * 3 * dims->D * 4);
 }
 
 sdm_status sdm_block_norm_backward(const sdm_norm_dims* dims, const void* r, const void* f,
@@ -650,7 +659,7 @@ sdm_status sdm_block_norm_backward(const sdm_norm_dims* dims, const void* r, con
     a.dr_out = dr_out, a.dn = dn;
     a.dr = dr, a.df = df, a.dgate = dgate;
     a.part = static_cast<float*>(ws);
-    const unsigned grid = (unsigned)std::min<long long>(dims->rows, kNormBwdBlocks);
+    const unsigned grid = norm_blocks(dims, true);
     if (grid > 0) {
         launch_norm_any(a, true, grid, stream);
         if ((e = launched())) return e;

@@ -161,6 +161,13 @@ SDM_DEV f32x2 silu2(f32x2 x) {
     return mul2(x, rcp_pair(add2(e, dup2(1.f))));
 }
 
+// d/dx (x sigmoid(x)) = s + x s (1 - s) of two values, s = sigmoid(x).
+SDM_DEV f32x2 dsilu2(f32x2 x) {
+    const f32x2 s = rcp_pair(add2(exp2_pair(mul2(x, dup2(-kLog2e))), dup2(1.f)));
+    const f32x2 r = fma2(s, dup2(-1.f), dup2(1.f));
+    return fma2(mul2(x, s), r, s);
+}
+
 // log(1 + e^x) = max(x, 0) + log(1 + e), e = e^-|x| <= 1, to a few units in the last place: a
 // step's relative error goes into every state and gradient behind it, so small steps (x << 0)
 // keep theirs.  log(1 + e) = 2 atanh(w), w = e / (2 + e) <= 1/3; 2 atanh(w) / w is a polynomial of
