@@ -6,23 +6,31 @@
 //   dp = do scale sigmoid(gate),  q = dp w_post,  df = rf (q - f^ mean(q f^))
 //   dgate = do scale p s (1-s),  dscale = sum do s p,  dw_post = sum dp f^,  dw_pre = sum dn o^
 //
-// Bound by memory.  A block takes whole rows, each read once into registers (so r_out may be r)
-// and normalised in place; the weights come from L1 after the first row.  The two sums of a row
-// (four in the gradient, two of them together) are block reductions in fp32.  What hides the
-// loads' latency: two blocks an SM that wait in turn, or (gradient, whose registers allow only
-// one) the next row's loads issued ahead.
+// Bound by memory.  A block of at most 512 threads takes whole rows of up to 4096 columns, wider
+// rows a cluster of two or four blocks, 4096 columns each; a row is read once into registers (so
+// r_out may be r) and normalised in place, eight values a thread as pairs (f32x2); the weights come
+// from L1 after the first row.  The two sums of a row (four in the gradient, two of them together)
+// are sums over the block's warps in fp32, over all of a cluster's warps through distributed shared
+// memory.  What hides the loads' latency: two blocks an SM that wait in turn, or (gradient, whose
+// registers allow only one) the next row's loads issued ahead.
 #pragma once
+
+#include <cooperative_groups.h>
 
 #include "ssm_util.cuh"
 
 namespace sdm {
 namespace ssm {
 
+constexpr int NORM_THREADS = 512;
+constexpr int NORM_COLS = 4096;  // columns of a block
+constexpr int NORM_MAXCL = 4;    // blocks of a cluster
+
 struct NormArgs {
     const void *r, *f, *gate, *dr_out, *dn;
     void *r_out, *n, *dr, *df, *dgate;  // r_out, n: forward
     const float *w_post, *scale, *w_pre;
-    float* part;  // backward: [gridDim.x][3][D] (dscale, dw_post, dw_pre)
+    float* part;  // backward: [row groups][3][D] (dscale, dw_post, dw_pre)
     long long rows;
     int D, rb, fb, xb;  // 1: bf16
     float eps;
@@ -32,12 +40,13 @@ struct NormArgs {
 // in flight before the first is waited for.
 template <int V>
 struct NormRaw {
+    static constexpr int N = (V + 1) / 2;
     uint32_t x[V];
     SDM_DEV void clear() {
 #pragma unroll
         for (int i = 0; i < V; ++i) x[i] = 0u;
     }
-    SDM_DEV void load(const void* p, int is_bf16, long long at) {
+    SDM_DEV void load(const void* p, bool is_bf16, long long at) {
         if constexpr (V == 4) {
             if (is_bf16) {
                 const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const bf16*>(p) + at);
@@ -50,270 +59,339 @@ struct NormRaw {
             x[0] = is_bf16 ? static_cast<const uint16_t*>(p)[at] : static_cast<const uint32_t*>(p)[at];
         }
     }
-    SDM_DEV void get(int is_bf16, float (&v)[V]) const {
+    SDM_DEV void get(bool is_bf16, f32x2 (&v)[N]) const {
         if constexpr (V == 4) {
-            v[0] = is_bf16 ? bf16_lo(x[0]) : __uint_as_float(x[0]);
-            v[1] = is_bf16 ? bf16_hi(x[0]) : __uint_as_float(x[1]);
-            v[2] = is_bf16 ? bf16_lo(x[1]) : __uint_as_float(x[2]);
-            v[3] = is_bf16 ? bf16_hi(x[1]) : __uint_as_float(x[3]);
+            v[0] = is_bf16 ? pack2(bf16_lo(x[0]), bf16_hi(x[0]))
+                           : pack2(__uint_as_float(x[0]), __uint_as_float(x[1]));
+            v[1] = is_bf16 ? pack2(bf16_lo(x[1]), bf16_hi(x[1]))
+                           : pack2(__uint_as_float(x[2]), __uint_as_float(x[3]));
         } else {
-            v[0] = is_bf16 ? bf16_lo(x[0]) : __uint_as_float(x[0]);
+            v[0] = pack2(is_bf16 ? bf16_lo(x[0]) : __uint_as_float(x[0]), 0.f);
         }
     }
 };
 template <int V>
-SDM_DEV void norm_store(void* p, int is_bf16, long long at, const float (&v)[V]) {
-    if (is_bf16) Vec<V>::store(static_cast<bf16*>(p) + at, v);
-    else Vec<V>::store(static_cast<float*>(p) + at, v);
+SDM_DEV void norm_store(void* p, bool is_bf16, long long at, const f32x2 (&v)[(V + 1) / 2]) {
+    float x[(V + 1) / 2 * 2], y[V];
+#pragma unroll
+    for (int i = 0; i < (V + 1) / 2; ++i) unpack2(v[i], x[2 * i], x[2 * i + 1]);
+#pragma unroll
+    for (int i = 0; i < V; ++i) y[i] = x[i];
+    if (is_bf16) Vec<V>::store(static_cast<bf16*>(p) + at, y);
+    else Vec<V>::store(static_cast<float*>(p) + at, y);
 }
-// V entries of a weight vector (1 where there is none), from L1 after the block's first row.
+// V entries of a weight vector (1 where there is none).
 template <int V>
-SDM_DEV void norm_weight(const float* w, int c, float (&v)[V]) {
+SDM_DEV void norm_weight(const float* w, int c, f32x2 (&v)[(V + 1) / 2]) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = 1.f;
-    if (w) Vec<V>::load(w + c, v);
-}
-
-// Sums of K values over the block (every thread gets them).  The slot alternates from one
-// reduction to the next, so that one barrier each is enough: a slot is written again only
-// behind the barrier of the reduction after the one that read it.
-template <int K>
-SDM_DEV void block_sum(float (&v)[K], float (*s)[2][32], int& slot) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-#pragma unroll
-    for (int k = 0; k < K; ++k) v[k] = warp_sum(v[k]);
-    if (nw == 1) return;
-    if (lane == 0) {
-#pragma unroll
-        for (int k = 0; k < K; ++k) s[slot][k][warp] = v[k];
+    for (int i = 0; i < (V + 1) / 2; ++i) v[i] = dup2(1.f);
+    if (!w) return;
+    if constexpr (V == 4) {
+        const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(w + c);
+        v[0] = x.x, v[1] = x.y;
+    } else {
+        v[0] = pack2(w[c], 0.f);
     }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < K; ++k) v[k] = warp_sum(lane < nw ? s[slot][k][lane] : 0.f);
-    slot ^= 1;
+}
+SDM_DEV float sum2(f32x2 v) {
+    float lo, hi;
+    unpack2(v, lo, hi);
+    return lo + hi;
+}
+SDM_DEV f32x2 sigmoid2(f32x2 x) {
+    return rcp_pair(add2(exp2_pair(mul2(x, dup2(-kLog2e))), dup2(1.f)));
 }
 
-// Element i of thread t is column (i*blockDim + t)*V.
-template <int V, int P>
-__global__ void __launch_bounds__(512, P * V <= 8 ? 2 : 1) block_norm_kernel(NormArgs a) {
-    __shared__ float s_sum[2][2][32];
-    int slot = 0;
+// Sums over a row's blocks, which alternate between two slots: one barrier each is enough, since a
+// slot is written again only behind the barrier of the reduction after the one that read it.
+template <bool CL>
+struct RowSum {
+    float (*s)[2][NORM_MAXCL * 16];
+    int slot, rank, ranks;
+    // v[0..K) to every thread
+    template <int K>
+    SDM_DEV void sum(float (&v)[K]) {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+#pragma unroll
+        for (int k = 0; k < K; ++k) v[k] = warp_sum(v[k]);
+        if (CL) {
+            namespace cg = cooperative_groups;
+            cg::cluster_group c = cg::this_cluster();
+            if (lane < ranks) {  // a lane a block: the warp's sum to each
+#pragma unroll
+                for (int k = 0; k < K; ++k)
+                    *c.map_shared_rank(&s[slot][k][rank * nw + warp], lane) = v[k];
+            }
+            c.sync();
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                float t = lane < ranks * nw ? s[slot][k][lane] : 0.f;
+                if (lane + 32 < ranks * nw) t += s[slot][k][lane + 32];
+                v[k] = warp_sum(t);
+            }
+        } else {
+            if (nw == 1) return;
+            if (lane == 0) {
+#pragma unroll
+                for (int k = 0; k < K; ++k) s[slot][k][warp] = v[k];
+            }
+            __syncthreads();
+#pragma unroll
+            for (int k = 0; k < K; ++k) v[k] = warp_sum(lane < nw ? s[slot][k][lane] : 0.f);
+        }
+        slot ^= 1;
+    }
+};
+
+// A block's place: its first column, the first row of its cluster and the rows' stride.
+template <bool CL>
+struct NormPlace {
+    int rank, ranks, col0;
+    long long first, step;
+    SDM_DEV NormPlace() {
+        ranks = 1, rank = 0;
+        if (CL) {
+            ranks = (int)cooperative_groups::this_cluster().num_blocks();
+            rank = (int)cooperative_groups::this_cluster().block_rank();
+        }
+        col0 = rank * NORM_COLS;
+        first = blockIdx.x / ranks;
+        step = gridDim.x / ranks;
+    }
+};
+
+// Piece i of thread t is column col0 + (i*blockDim + t)*V.  DT: which of r, f, x are bf16 (bits 0,
+// 1, 2), or -1: as the arguments say.
+template <int V, int P, bool CL, int DT>
+__global__ void __launch_bounds__(NORM_THREADS, 2) block_norm_kernel(NormArgs a) {
+    constexpr int N = (V + 1) / 2;
+    __shared__ float s_sum[2][2][NORM_MAXCL * 16];
+    const bool rb = DT < 0 ? a.rb : DT & 1, fb = DT < 0 ? a.fb : DT & 2, xb = DT < 0 ? a.xb : DT & 4;
+    const NormPlace<CL> at;
+    RowSum<CL> red{s_sum, 0, at.rank, at.ranks};
     const float inv_d = 1.f / (float)a.D;
-    for (long long row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    for (long long row = at.first; row < a.rows; row += at.step) {
         const long long base = row * a.D;
         NormRaw<V> rf[P], rr[P], rg[P];
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-            const int c = (i * blockDim.x + threadIdx.x) * V;
+            const int c = at.col0 + (i * blockDim.x + threadIdx.x) * V;
             rf[i].clear();
             rr[i].clear();
             rg[i].clear();
             if (c < a.D) {
-                rf[i].load(a.f, a.fb, base + c);
-                rr[i].load(a.r, a.rb, base + c);
-                if (a.gate) rg[i].load(a.gate, a.xb, base + c);
+                rf[i].load(a.f, fb, base + c);
+                rr[i].load(a.r, rb, base + c);
+                if (a.gate) rg[i].load(a.gate, xb, base + c);
             }
         }
-        float f[P][V], o[P][V];
-        float ss[1] = {0.f};
+        f32x2 f[P][N], o[P][N], s2 = dup2(0.f);
+        float ss[1];
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-            rf[i].get(a.fb, f[i]);
+            rf[i].get(fb, f[i]);
 #pragma unroll
-            for (int v = 0; v < V; ++v) ss[0] = fmaf(f[i][v], f[i][v], ss[0]);
+            for (int v = 0; v < N; ++v) s2 = fma2(f[i][v], f[i][v], s2);
         }
-        float k = 1.f;
+        f32x2 k = dup2(1.f);
         if (a.w_post) {
-            block_sum<1>(ss, s_sum, slot);
-            k = rsqrtf(ss[0] * inv_d + a.eps);
+            ss[0] = sum2(s2);
+            red.sum(ss);
+            k = dup2(rsqrtf(ss[0] * inv_d + a.eps));
         }
-        ss[0] = 0.f;
+        s2 = dup2(0.f);
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-            const int c = (i * blockDim.x + threadIdx.x) * V;
+            const int c = at.col0 + (i * blockDim.x + threadIdx.x) * V;
             if (c < a.D) {
-                float wp[V], sc[V], g[V];
+                f32x2 wp[N], sc[N], g[N];
                 norm_weight<V>(a.w_post, c, wp);
                 norm_weight<V>(a.scale, c, sc);
-                rg[i].get(a.xb, g);
-                rr[i].get(a.rb, o[i]);
+                rg[i].get(xb, g);
+                rr[i].get(rb, o[i]);
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    float m = sc[v] * wp[v] * k;
-                    if (a.gate) m *= sigmoid(g[v]);
-                    o[i][v] = fmaf(m, f[i][v], o[i][v]);
-                    ss[0] = fmaf(o[i][v], o[i][v], ss[0]);
+                for (int v = 0; v < N; ++v) {
+                    f32x2 m = mul2(mul2(sc[v], wp[v]), k);
+                    if (a.gate) m = mul2(m, sigmoid2(g[v]));
+                    o[i][v] = fma2(m, f[i][v], o[i][v]);
+                    s2 = fma2(o[i][v], o[i][v], s2);
                 }
-                if (a.r_out) norm_store<V>(a.r_out, a.rb, base + c, o[i]);
+                if (a.r_out) norm_store<V>(a.r_out, rb, base + c, o[i]);
             }
         }
         if (!a.n) continue;
-        block_sum<1>(ss, s_sum, slot);
-        const float ro = rsqrtf(ss[0] * inv_d + a.eps);
+        ss[0] = sum2(s2);
+        red.sum(ss);
+        k = dup2(rsqrtf(ss[0] * inv_d + a.eps));
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-            const int c = (i * blockDim.x + threadIdx.x) * V;
+            const int c = at.col0 + (i * blockDim.x + threadIdx.x) * V;
             if (c < a.D) {
-                float wq[V];
+                f32x2 wq[N];
                 norm_weight<V>(a.w_pre, c, wq);
 #pragma unroll
-                for (int v = 0; v < V; ++v) o[i][v] *= ro * wq[v];
-                norm_store<V>(a.n, a.xb, base + c, o[i]);
+                for (int v = 0; v < N; ++v) o[i][v] = mul2(o[i][v], mul2(k, wq[v]));
+                norm_store<V>(a.n, xb, base + c, o[i]);
             }
         }
     }
+    if (CL) cooperative_groups::this_cluster().sync();  // no block ends while others write to it
 }
 
-// The next row's loads are issued before this row's arithmetic, so that one block an SM keeps
-// memory busy.
-template <int V, int P>
-__global__ void __launch_bounds__(512, 1) block_norm_bwd_kernel(NormArgs a) {
-    __shared__ float s_sum[2][2][32];
-    int slot = 0;
-    float aw[P][V], as[P][V], aq[P][V];
+template <int V, int P, bool CL, int DT>
+__global__ void __launch_bounds__(NORM_THREADS, 1) block_norm_bwd_kernel(NormArgs a) {
+    constexpr int N = (V + 1) / 2;
+    __shared__ float s_sum[2][2][NORM_MAXCL * 16];
+    const bool rb = DT < 0 ? a.rb : DT & 1, fb = DT < 0 ? a.fb : DT & 2, xb = DT < 0 ? a.xb : DT & 4;
+    const NormPlace<CL> at;
+    RowSum<CL> red{s_sum, 0, at.rank, at.ranks};
+    const f32x2 one = dup2(1.f), zero = dup2(0.f);
+    f32x2 aw[P][N], as[P][N], aq[P][N];
 #pragma unroll
     for (int i = 0; i < P; ++i)
 #pragma unroll
-        for (int v = 0; v < V; ++v) aw[i][v] = as[i][v] = aq[i][v] = 0.f;
+        for (int v = 0; v < N; ++v) aw[i][v] = as[i][v] = aq[i][v] = zero;
     const float inv_d = 1.f / (float)a.D;
     NormRaw<V> rf[P], rr[P], rg[P], rn[P], rd[P];
     auto fetch = [&](long long row) {
         const long long base = row * a.D;
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-            const int c = (i * blockDim.x + threadIdx.x) * V;
+            const int c = at.col0 + (i * blockDim.x + threadIdx.x) * V;
             rf[i].clear();
             rr[i].clear();
             rg[i].clear();
             rn[i].clear();
             rd[i].clear();
             if (c < a.D && row < a.rows) {
-                rf[i].load(a.f, a.fb, base + c);
-                rr[i].load(a.r, a.rb, base + c);
-                if (a.gate) rg[i].load(a.gate, a.xb, base + c);
-                if (a.dn) rn[i].load(a.dn, a.xb, base + c);
-                if (a.dr_out) rd[i].load(a.dr_out, a.rb, base + c);
+                rf[i].load(a.f, fb, base + c);
+                rr[i].load(a.r, rb, base + c);
+                if (a.gate) rg[i].load(a.gate, xb, base + c);
+                if (a.dn) rn[i].load(a.dn, xb, base + c);
+                if (a.dr_out) rd[i].load(a.dr_out, rb, base + c);
             }
         }
     };
-    fetch(blockIdx.x);
-    for (long long row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    fetch(at.first);
+    for (long long row = at.first; row < a.rows; row += at.step) {
         const long long base = row * a.D;
-        float f[P][V], o[P][V], g[P][V], dn[P][V], dr[P][V];
-        float ss[1] = {0.f};
+        f32x2 f[P][N], o[P][N], g[P][N], dn[P][N], dr[P][N], s2 = zero, t2 = zero;
+        float ss[1], st[2];
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-            rf[i].get(a.fb, f[i]);
-            rr[i].get(a.rb, o[i]);
-            rg[i].get(a.xb, g[i]);
-            rn[i].get(a.xb, dn[i]);
-            rd[i].get(a.rb, dr[i]);
+            rf[i].get(fb, f[i]);
+            rr[i].get(rb, o[i]);
+            rg[i].get(xb, g[i]);
+            rn[i].get(xb, dn[i]);
+            rd[i].get(rb, dr[i]);
 #pragma unroll
-            for (int v = 0; v < V; ++v) ss[0] = fmaf(f[i][v], f[i][v], ss[0]);
+            for (int v = 0; v < N; ++v) s2 = fma2(f[i][v], f[i][v], s2);
         }
-        fetch(row + gridDim.x);
-        float rf1 = 1.f;
+        fetch(row + at.step);
+        f32x2 rf1 = one;
         if (a.w_post) {
-            block_sum<1>(ss, s_sum, slot);
-            rf1 = rsqrtf(ss[0] * inv_d + a.eps);
+            ss[0] = sum2(s2);
+            red.sum(ss);
+            rf1 = dup2(rsqrtf(ss[0] * inv_d + a.eps));
         }
         // f becomes f^ (f itself without the norm), g the gate's sigmoid
-        float s2[2] = {0.f, 0.f};
+        s2 = zero;
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-            const int c = (i * blockDim.x + threadIdx.x) * V;
+            const int c = at.col0 + (i * blockDim.x + threadIdx.x) * V;
             if (c >= a.D) continue;
-            float wp[V], sc[V], wq[V];
+            f32x2 wp[N], sc[N], wq[N];
             norm_weight<V>(a.w_post, c, wp);
             norm_weight<V>(a.scale, c, sc);
             norm_weight<V>(a.w_pre, c, wq);
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                f[i][v] *= rf1;
-                g[i][v] = a.gate ? sigmoid(g[i][v]) : 1.f;
-                o[i][v] = fmaf(sc[v] * g[i][v], f[i][v] * wp[v], o[i][v]);
-                s2[0] = fmaf(o[i][v], o[i][v], s2[0]);
-                s2[1] = fmaf(o[i][v] * wq[v], dn[i][v], s2[1]);
+            for (int v = 0; v < N; ++v) {
+                f[i][v] = mul2(f[i][v], rf1);
+                g[i][v] = a.gate ? sigmoid2(g[i][v]) : one;
+                o[i][v] = fma2(mul2(sc[v], g[i][v]), mul2(f[i][v], wp[v]), o[i][v]);
+                s2 = fma2(o[i][v], o[i][v], s2);
+                t2 = fma2(mul2(o[i][v], wq[v]), dn[i][v], t2);
             }
         }
-        float ro = 0.f, mo = 0.f;
+        f32x2 ro = zero, mo = zero;
         if (a.dn) {
-            block_sum<2>(s2, s_sum, slot);
-            ro = rsqrtf(s2[0] * inv_d + a.eps);
-            mo = s2[1] * ro * inv_d;  // mean(m o^)
+            st[0] = sum2(s2), st[1] = sum2(t2);
+            red.sum(st);
+            const float q = rsqrtf(st[0] * inv_d + a.eps);
+            ro = dup2(q);
+            mo = dup2(-(st[1] * q * inv_d));  // -mean(m o^)
         }
-        float sq[1] = {0.f};
+        s2 = zero;
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-            const int c = (i * blockDim.x + threadIdx.x) * V;
+            const int c = at.col0 + (i * blockDim.x + threadIdx.x) * V;
             if (c >= a.D) continue;
-            float wp[V], sc[V], wq[V], dg[V];
+            f32x2 wp[N], sc[N], wq[N], dg[N];
             norm_weight<V>(a.w_post, c, wp);
             norm_weight<V>(a.scale, c, sc);
             norm_weight<V>(a.w_pre, c, wq);
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const float oh = o[i][v] * ro;
-                aq[i][v] = fmaf(dn[i][v], oh, aq[i][v]);
-                const float d = fmaf(ro, fmaf(dn[i][v], wq[v], -oh * mo), dr[i][v]);
+            for (int v = 0; v < N; ++v) {
+                const f32x2 oh = mul2(o[i][v], ro);
+                aq[i][v] = fma2(dn[i][v], oh, aq[i][v]);
+                const f32x2 d = fma2(ro, fma2(dn[i][v], wq[v], mul2(oh, mo)), dr[i][v]);
                 dr[i][v] = d;
-                const float p = f[i][v] * wp[v], dsp = d * p * g[i][v];
-                as[i][v] += dsp;
-                dg[v] = dsp * sc[v] * (1.f - g[i][v]);
-                const float dp = d * sc[v] * g[i][v];
-                aw[i][v] = fmaf(dp, f[i][v], aw[i][v]);
-                o[i][v] = dp * wp[v];  // q
-                sq[0] = fmaf(o[i][v], f[i][v], sq[0]);
+                const f32x2 ds = mul2(d, g[i][v]);         // do sigmoid(gate)
+                const f32x2 dsp = mul2(ds, mul2(f[i][v], wp[v]));
+                as[i][v] = add2(as[i][v], dsp);
+                dg[v] = mul2(mul2(dsp, sc[v]), fma2(g[i][v], dup2(-1.f), one));
+                const f32x2 dp = mul2(ds, sc[v]);
+                aw[i][v] = fma2(dp, f[i][v], aw[i][v]);
+                o[i][v] = mul2(dp, wp[v]);  // q
+                s2 = fma2(o[i][v], f[i][v], s2);
             }
-            if (a.dr) norm_store<V>(a.dr, a.rb, base + c, dr[i]);
-            if (a.dgate) norm_store<V>(a.dgate, a.xb, base + c, dg);
+            if (a.dr) norm_store<V>(a.dr, rb, base + c, dr[i]);
+            if (a.dgate) norm_store<V>(a.dgate, xb, base + c, dg);
         }
-        float mf = 0.f;
+        f32x2 mf = zero;
         if (a.w_post) {
-            block_sum<1>(sq, s_sum, slot);
-            mf = sq[0] * inv_d;
+            ss[0] = sum2(s2);
+            red.sum(ss);
+            mf = dup2(-(ss[0] * inv_d));
         }
         if (a.df) {
 #pragma unroll
             for (int i = 0; i < P; ++i) {
-                const int c = (i * blockDim.x + threadIdx.x) * V;
+                const int c = at.col0 + (i * blockDim.x + threadIdx.x) * V;
                 if (c >= a.D) continue;
 #pragma unroll
-                for (int v = 0; v < V; ++v) o[i][v] = rf1 * (o[i][v] - f[i][v] * mf);
-                norm_store<V>(a.df, a.fb, base + c, o[i]);
+                for (int v = 0; v < N; ++v) o[i][v] = mul2(rf1, fma2(f[i][v], mf, o[i][v]));
+                norm_store<V>(a.df, fb, base + c, o[i]);
             }
         }
     }
-    float* part = a.part + (long long)blockIdx.x * 3 * a.D;
+    float* part = a.part + at.first * 3 * a.D;
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-        const int c = (i * blockDim.x + threadIdx.x) * V;
-        if (c < a.D) {
-            Vec<V>::store(part + c, as[i]);
-            if constexpr (V == 4) {
-                Vec<V>::store(part + a.D + c, aw[i]);  // D is a multiple of 4
-                Vec<V>::store(part + 2 * a.D + c, aq[i]);
-            } else {
-                part[a.D + c] = aw[i][0];
-                part[2 * a.D + c] = aq[i][0];
-            }
+        const int c = at.col0 + (i * blockDim.x + threadIdx.x) * V;
+        if (c < a.D) {  // V = 4: D is a multiple of 4
+            norm_store<V>(part, false, c, as[i]);
+            norm_store<V>(part, false, (long long)a.D + c, aw[i]);
+            norm_store<V>(part, false, 2LL * a.D + c, aq[i]);
         }
     }
+    if (CL) cooperative_groups::this_cluster().sync();
 }
 
-// out[k][c] = the blocks' shares in order, k: dscale, dw_post, dw_pre.  One warp row of 32
-// columns per 8 segments of blocks, the segments added in order.
+// out[k][c] = the row groups' shares in a fixed order, k: dscale, dw_post, dw_pre: eight interleaved
+// segments of shares, then the segments.
 constexpr int SUM_SEG = 8;
-__global__ void __launch_bounds__(32 * SUM_SEG) norm_sum_kernel(const float* part, int blocks,
+__global__ void __launch_bounds__(32 * SUM_SEG) norm_sum_kernel(const float* part, int shares,
                                                                 int D, float* dscale,
                                                                 float* dw_post, float* dw_pre) {
     __shared__ float s[SUM_SEG][32];
     const int lane = threadIdx.x & 31, seg = threadIdx.x >> 5;
     const long long e = (long long)blockIdx.x * 32 + lane, n = 3LL * D;
-    const int per = (blocks + SUM_SEG - 1) / SUM_SEG;
     float sum = 0.f;
-    if (e < n)
-        for (int p = seg * per; p < min(blocks, (seg + 1) * per); ++p) sum += part[p * n + e];
+    if (e < n) {
+#pragma unroll 4
+        for (int p = seg; p < shares; p += SUM_SEG) sum += part[p * n + e];
+    }
     s[seg][lane] = sum;
     __syncthreads();
     if (seg == 0 && e < n) {

@@ -450,7 +450,6 @@ sdm_status check_scan_in(const sdm_scan_dims* d, const sdm_view* u, const sdm_vi
 }
 
 // ---- block norms ---------------------------------------------------------------------------
-constexpr int kNormThreads = 512;
 
 sdm_status check_norm(const sdm_norm_dims* d) {
     if (!d) return SDM_ERR_ARG;
@@ -470,36 +469,56 @@ NormArgs norm_args(const sdm_norm_dims* d, const void* r, const void* f, const f
     return a;
 }
 
-// Threads of a block whose threads take P pieces of V values.
-unsigned norm_threads(int D, int V, int P) {
-    return (unsigned)(ceil_div(ceil_div(ceil_div(D, V), P), 32) * 32);
+struct NormPlan {
+    unsigned threads, blocks;  // blocks of a row: 1, 2 or 4
+    unsigned groups;           // rows in work at a time
+};
+
+// Eight values a thread, 4096 columns a block.  The forward pass keeps 1024 threads of blocks an SM
+// (16 blocks at most), the gradient 512, so that few shares of its sums are written.
+NormPlan norm_plan(const sdm_norm_dims* d, bool bwd) {
+    NormPlan p;
+    const int cols = std::min(d->D, NORM_COLS);
+    p.threads = (unsigned)(ceil_div(ceil_div(cols, 8), 32) * 32);
+    p.blocks = d->D <= NORM_COLS ? 1 : (d->D <= 2 * NORM_COLS ? 2 : 4);
+    const long long per_sm = std::min<long long>(16, (bwd ? 512 : 1024) / p.threads);
+    p.groups = (unsigned)std::min<long long>(d->rows, std::max(1LL, kSms * per_sm / p.blocks));
+    return p;
 }
 
-// Blocks: the forward pass two an SM (more where they are small), the gradient one of at most 512
-// threads, so that few shares of the sums are written.
-unsigned norm_blocks(const sdm_norm_dims* d, bool bwd) {
-    const int V = d->D % 4 == 0 ? 4 : 1;
-    const unsigned nt = norm_threads(d->D, V, V == 4 ? 2 : 8);
-    const long long per_sm = std::max<long long>(1, (bwd ? 512 : 1024) / nt);
-    return (unsigned)std::min<long long>(d->rows, kSms * std::min<long long>(per_sm, 16));
+template <int V, bool CL, int DT>
+sdm_status launch_norm(const NormArgs& a, bool bwd, const NormPlan& p, cudaStream_t s) {
+    constexpr int P = 8 / V;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = p.blocks, attr.val.clusterDim.y = 1, attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(p.groups * p.blocks);
+    cfg.blockDim = dim3(p.threads);
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = CL ? 1 : 0;
+    const cudaError_t e = bwd ? cudaLaunchKernelEx(&cfg, block_norm_bwd_kernel<V, P, CL, DT>, a)
+                              : cudaLaunchKernelEx(&cfg, block_norm_kernel<V, P, CL, DT>, a);
+    (void)cudaGetLastError();
+    return e == cudaSuccess ? SDM_OK : SDM_ERR_CUDA;
 }
 
-template <int V, int P>
-void launch_norm(const NormArgs& a, bool bwd, unsigned grid, cudaStream_t s) {
-    const unsigned nt = norm_threads(a.D, V, P);
-    if (bwd) block_norm_bwd_kernel<V, P><<<grid, nt, 0, s>>>(a);
-    else block_norm_kernel<V, P><<<grid, nt, 0, s>>>(a);
-}
-
-// Pieces of a thread: as few as fit a row into 512 threads.
-void launch_norm_any(const NormArgs& a, bool bwd, unsigned grid, cudaStream_t s) {
-    if (a.D % 4 == 0) {
-        if (a.D <= 2 * 4 * kNormThreads) return launch_norm<4, 2>(a, bwd, grid, s);
-        if (a.D <= 4 * 4 * kNormThreads) return launch_norm<4, 4>(a, bwd, grid, s);
-        return launch_norm<4, 8>(a, bwd, grid, s);
+sdm_status launch_norm_any(const NormArgs& a, bool bwd, const NormPlan& p, cudaStream_t s) {
+    if (a.D % 4 != 0)
+        return p.blocks > 1 ? launch_norm<1, true, -1>(a, bwd, p, s)
+                            : launch_norm<1, false, -1>(a, bwd, p, s);
+    if (p.blocks > 1) return launch_norm<4, true, -1>(a, bwd, p, s);
+    switch (a.rb | a.fb << 1 | a.xb << 2) {
+        case 0: return launch_norm<4, false, 0>(a, bwd, p, s);
+        case 1: return launch_norm<4, false, 1>(a, bwd, p, s);
+        case 2: return launch_norm<4, false, 2>(a, bwd, p, s);
+        case 3: return launch_norm<4, false, 3>(a, bwd, p, s);
+        case 4: return launch_norm<4, false, 4>(a, bwd, p, s);
+        case 5: return launch_norm<4, false, 5>(a, bwd, p, s);
+        case 6: return launch_norm<4, false, 6>(a, bwd, p, s);
+        default: return launch_norm<4, false, 7>(a, bwd, p, s);
     }
-    if (a.D <= 8 * kNormThreads) return launch_norm<1, 8>(a, bwd, grid, s);
-    return launch_norm<1, 32>(a, bwd, grid, s);
 }
 
 }  // namespace
@@ -631,13 +650,12 @@ sdm_status sdm_block_norm(const sdm_norm_dims* dims, const void* r, const void* 
     if (dims->rows == 0) return SDM_OK;
     NormArgs a = norm_args(dims, r, f, w_post, gate, scale, w_pre);
     a.r_out = r_out, a.n = n;
-    launch_norm_any(a, false, norm_blocks(dims, false), stream);
-    return launched();
+    return launch_norm_any(a, false, norm_plan(dims, false), stream);
 }
 
 size_t sdm_block_norm_backward_workspace_bytes(const sdm_norm_dims* dims) {
     if (check_norm(dims) != SDM_OK) return 0;
-    return up256(std::max<size_t>(1, norm_blocks(dims, true)) * 3 * dims->D * 4);
+    return up256(std::max<size_t>(1, norm_plan(dims, true).groups) * 3 * dims->D * 4);
 }
 
 sdm_status sdm_block_norm_backward(const sdm_norm_dims* dims, const void* r, const void* f,
@@ -659,13 +677,10 @@ sdm_status sdm_block_norm_backward(const sdm_norm_dims* dims, const void* r, con
     a.dr_out = dr_out, a.dn = dn;
     a.dr = dr, a.df = df, a.dgate = dgate;
     a.part = static_cast<float*>(ws);
-    const unsigned grid = norm_blocks(dims, true);
-    if (grid > 0) {
-        launch_norm_any(a, true, grid, stream);
-        if ((e = launched())) return e;
-    }
+    const NormPlan p = norm_plan(dims, true);
+    if (dims->rows > 0 && (e = launch_norm_any(a, true, p, stream))) return e;
     norm_sum_kernel<<<(unsigned)ceil_div(3LL * dims->D, 32), 32 * SUM_SEG, 0, stream>>>(
-        a.part, (int)grid, dims->D, dscale, dw_post, dw_pre);
+        a.part, (int)p.groups, dims->D, dscale, dw_post, dw_pre);
     return launched();
 }
 
