@@ -9,8 +9,8 @@
 // Bound by memory.  A block of at most 512 threads takes whole rows of up to 4096 columns, wider
 // rows a cluster of two or four blocks, 4096 columns each; a row is read once into registers (so
 // r_out may be r) and normalised in place, eight values a thread as pairs (f32x2); the weights come
-// from L1 after the first row.  The two sums of a row (four in the gradient, two of them together)
-// are sums over the block's warps in fp32, over all of a cluster's warps through distributed shared
+// from L1 after the first row.  The sums of a row (two reductions; the gradient one, see there) are
+// sums over the block's warps in fp32, over all of a cluster's warps through distributed shared
 // memory.  What hides the loads' latency: two blocks an SM that wait in turn, or (gradient, whose
 // registers allow only one) the next row's loads issued ahead.
 #pragma once
@@ -104,41 +104,70 @@ SDM_DEV f32x2 sigmoid2(f32x2 x) {
 
 // Sums over a row's blocks, which alternate between two slots: one barrier each is enough, since a
 // slot is written again only behind the barrier of the reduction after the one that read it.
+constexpr int NORM_SUMS = 8;
+struct NormSums {
+    float s[2][NORM_SUMS][NORM_MAXCL * 16];  // of every warp; zero where there is none
+    SDM_DEV void clear() {
+        float* p = &s[0][0][0];
+        for (int i = threadIdx.x; i < 2 * NORM_SUMS * NORM_MAXCL * 16; i += blockDim.x) p[i] = 0.f;
+    }
+};
 template <bool CL>
 struct RowSum {
-    float (*s)[2][NORM_MAXCL * 16];
+    NormSums& m;
     int slot, rank, ranks;
-    // v[0..K) to every thread
+    SDM_DEV void barrier() const {
+        if (CL) cooperative_groups::this_cluster().sync();
+        else __syncthreads();
+    }
+    // v[0..K) to every thread: over the lanes by shuffles that halve the values with each step, lane
+    // i ending with value i; over the warps four lanes a value.
     template <int K>
     SDM_DEV void sum(float (&v)[K]) {
-        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+        static_assert(K <= NORM_SUMS, "sums");
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        float x[NORM_SUMS];
 #pragma unroll
-        for (int k = 0; k < K; ++k) v[k] = warp_sum(v[k]);
-        if (CL) {
-            namespace cg = cooperative_groups;
-            cg::cluster_group c = cg::this_cluster();
-            if (lane < ranks) {  // a lane a block: the warp's sum to each
-#pragma unroll
-                for (int k = 0; k < K; ++k)
-                    *c.map_shared_rank(&s[slot][k][rank * nw + warp], lane) = v[k];
-            }
-            c.sync();
-#pragma unroll
-            for (int k = 0; k < K; ++k) {
-                float t = lane < ranks * nw ? s[slot][k][lane] : 0.f;
-                if (lane + 32 < ranks * nw) t += s[slot][k][lane + 32];
-                v[k] = warp_sum(t);
-            }
+        for (int k = 0; k < NORM_SUMS; ++k) x[k] = k < K ? v[k < K ? k : 0] : 0.f;
+        if (K == 1) {
+            x[0] = warp_sum(x[0]);
         } else {
-            if (nw == 1) return;
-            if (lane == 0) {
+            int cnt = NORM_SUMS;
 #pragma unroll
-                for (int k = 0; k < K; ++k) s[slot][k][warp] = v[k];
+            for (int bit = 1; bit < NORM_SUMS; bit <<= 1) {
+                cnt >>= 1;
+                const bool up = lane & bit;
+#pragma unroll
+                for (int k = 0; k < NORM_SUMS / 2; ++k)
+                    if (k < cnt) {
+                        const float mine = up ? x[2 * k + 1] : x[2 * k];
+                        const float other = up ? x[2 * k] : x[2 * k + 1];
+                        x[k] = mine + __shfl_xor_sync(0xffffffffu, other, bit);
+                    }
             }
-            __syncthreads();
-#pragma unroll
-            for (int k = 0; k < K; ++k) v[k] = warp_sum(lane < nw ? s[slot][k][lane] : 0.f);
+            x[0] += __shfl_xor_sync(0xffffffffu, x[0], 8);
+            x[0] += __shfl_xor_sync(0xffffffffu, x[0], 16);
         }
+        if (lane < K) {
+            float* to = &m.s[slot][lane][rank * 16 + warp];
+            if (CL) {
+                for (int q = 0; q < ranks; ++q) *cooperative_groups::this_cluster().map_shared_rank(to, q) = x[0];
+            } else {
+                *to = x[0];
+            }
+        }
+        barrier();
+        constexpr int PER = CL ? NORM_MAXCL * 4 : 4;  // warps a lane adds
+        float t = 0.f;
+#pragma unroll
+        for (int i = 0; i < PER; i += 4) {
+            const float4 q = *reinterpret_cast<const float4*>(&m.s[slot][lane >> 2][(lane & 3) * PER + i]);
+            t += (q.x + q.y) + (q.z + q.w);
+        }
+        t += __shfl_xor_sync(0xffffffffu, t, 1);
+        t += __shfl_xor_sync(0xffffffffu, t, 2);
+#pragma unroll
+        for (int k = 0; k < K; ++k) v[k] = __shfl_sync(0xffffffffu, t, 4 * k);
         slot ^= 1;
     }
 };
@@ -165,10 +194,12 @@ struct NormPlace {
 template <int V, int P, bool CL, int DT>
 __global__ void __launch_bounds__(NORM_THREADS, 2) block_norm_kernel(NormArgs a) {
     constexpr int N = (V + 1) / 2;
-    __shared__ float s_sum[2][2][NORM_MAXCL * 16];
+    __shared__ __align__(16) NormSums s_sum;
     const bool rb = DT < 0 ? a.rb : DT & 1, fb = DT < 0 ? a.fb : DT & 2, xb = DT < 0 ? a.xb : DT & 4;
     const NormPlace<CL> at;
     RowSum<CL> red{s_sum, 0, at.rank, at.ranks};
+    s_sum.clear();
+    red.barrier();
     const float inv_d = 1.f / (float)a.D;
     for (long long row = at.first; row < a.rows; row += at.step) {
         const long long base = row * a.D;
@@ -241,10 +272,12 @@ __global__ void __launch_bounds__(NORM_THREADS, 2) block_norm_kernel(NormArgs a)
 template <int V, int P, bool CL, int DT>
 __global__ void __launch_bounds__(NORM_THREADS, 1) block_norm_bwd_kernel(NormArgs a) {
     constexpr int N = (V + 1) / 2;
-    __shared__ float s_sum[2][2][NORM_MAXCL * 16];
+    __shared__ __align__(16) NormSums s_sum;
     const bool rb = DT < 0 ? a.rb : DT & 1, fb = DT < 0 ? a.fb : DT & 2, xb = DT < 0 ? a.xb : DT & 4;
     const NormPlace<CL> at;
     RowSum<CL> red{s_sum, 0, at.rank, at.ranks};
+    s_sum.clear();
+    red.barrier();
     const f32x2 one = dup2(1.f), zero = dup2(0.f);
     f32x2 aw[P][N], as[P][N], aq[P][N];
 #pragma unroll
@@ -273,10 +306,27 @@ __global__ void __launch_bounds__(NORM_THREADS, 1) block_norm_bwd_kernel(NormArg
         }
     };
     fetch(at.first);
+    // One reduction a row: the sum of the next row's f^2 goes with this row's.  What df needs of the
+    // row, mean(q f^) = mean(do a) with a = scale sigmoid(gate) p, follows from the sums of m a, o a
+    // and dr_out a, since do = dr_out + ro (m - o^ mean(m o^)).
+    auto square = [&]() {
+        f32x2 s2 = zero;
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            f32x2 f[N];
+            rf[i].get(fb, f);
+#pragma unroll
+            for (int v = 0; v < N; ++v) s2 = fma2(f[v], f[v], s2);
+        }
+        return sum2(s2);
+    };
+    float next[1] = {a.w_post ? square() : 0.f};
+    if (a.w_post) red.sum(next);
     for (long long row = at.first; row < a.rows; row += at.step) {
         const long long base = row * a.D;
-        f32x2 f[P][N], o[P][N], g[P][N], dn[P][N], dr[P][N], s2 = zero, t2 = zero;
-        float ss[1], st[2];
+        const f32x2 rf1 = a.w_post ? dup2(rsqrtf(next[0] * inv_d + a.eps)) : one;
+        f32x2 f[P][N], o[P][N], g[P][N], dn[P][N], dr[P][N];
+        f32x2 so = zero, sm = zero, sma = zero, soa = zero, sda = zero;
 #pragma unroll
         for (int i = 0; i < P; ++i) {
             rf[i].get(fb, f[i]);
@@ -284,18 +334,9 @@ __global__ void __launch_bounds__(NORM_THREADS, 1) block_norm_bwd_kernel(NormArg
             rg[i].get(xb, g[i]);
             rn[i].get(xb, dn[i]);
             rd[i].get(rb, dr[i]);
-#pragma unroll
-            for (int v = 0; v < N; ++v) s2 = fma2(f[i][v], f[i][v], s2);
         }
         fetch(row + at.step);
-        f32x2 rf1 = one;
-        if (a.w_post) {
-            ss[0] = sum2(s2);
-            red.sum(ss);
-            rf1 = dup2(rsqrtf(ss[0] * inv_d + a.eps));
-        }
         // f becomes f^ (f itself without the norm), g the gate's sigmoid
-        s2 = zero;
 #pragma unroll
         for (int i = 0; i < P; ++i) {
             const int c = at.col0 + (i * blockDim.x + threadIdx.x) * V;
@@ -308,20 +349,29 @@ __global__ void __launch_bounds__(NORM_THREADS, 1) block_norm_bwd_kernel(NormArg
             for (int v = 0; v < N; ++v) {
                 f[i][v] = mul2(f[i][v], rf1);
                 g[i][v] = a.gate ? sigmoid2(g[i][v]) : one;
-                o[i][v] = fma2(mul2(sc[v], g[i][v]), mul2(f[i][v], wp[v]), o[i][v]);
-                s2 = fma2(o[i][v], o[i][v], s2);
-                t2 = fma2(mul2(o[i][v], wq[v]), dn[i][v], t2);
+                const f32x2 k = mul2(mul2(sc[v], g[i][v]), mul2(f[i][v], wp[v])), m = mul2(dn[i][v], wq[v]);
+                o[i][v] = add2(k, o[i][v]);
+                so = fma2(o[i][v], o[i][v], so);
+                sm = fma2(o[i][v], m, sm);
+                sma = fma2(m, k, sma);
+                soa = fma2(o[i][v], k, soa);
+                sda = fma2(dr[i][v], k, sda);
             }
         }
-        f32x2 ro = zero, mo = zero;
-        if (a.dn) {
-            st[0] = sum2(s2), st[1] = sum2(t2);
+        f32x2 ro = zero, mo = zero, mf = zero;
+        if (a.dn || a.w_post) {
+            float st[6] = {sum2(so), sum2(sm), sum2(sma), sum2(soa), sum2(sda), a.w_post ? square() : 0.f};
             red.sum(st);
-            const float q = rsqrtf(st[0] * inv_d + a.eps);
+            next[0] = st[5];
+            float q = 0.f, mean = 0.f;
+            if (a.dn) {
+                q = rsqrtf(st[0] * inv_d + a.eps);
+                mean = st[1] * q * inv_d;  // mean(m o^)
+            }
             ro = dup2(q);
-            mo = dup2(-(st[1] * q * inv_d));  // -mean(m o^)
+            mo = dup2(-mean);
+            if (a.w_post) mf = dup2(-(st[4] + q * (st[2] - q * mean * st[3])) * inv_d);
         }
-        s2 = zero;
 #pragma unroll
         for (int i = 0; i < P; ++i) {
             const int c = at.col0 + (i * blockDim.x + threadIdx.x) * V;
@@ -336,33 +386,17 @@ __global__ void __launch_bounds__(NORM_THREADS, 1) block_norm_bwd_kernel(NormArg
                 aq[i][v] = fma2(dn[i][v], oh, aq[i][v]);
                 const f32x2 d = fma2(ro, fma2(dn[i][v], wq[v], mul2(oh, mo)), dr[i][v]);
                 dr[i][v] = d;
-                const f32x2 ds = mul2(d, g[i][v]);         // do sigmoid(gate)
+                const f32x2 ds = mul2(d, g[i][v]);  // do sigmoid(gate)
                 const f32x2 dsp = mul2(ds, mul2(f[i][v], wp[v]));
                 as[i][v] = add2(as[i][v], dsp);
                 dg[v] = mul2(mul2(dsp, sc[v]), fma2(g[i][v], dup2(-1.f), one));
                 const f32x2 dp = mul2(ds, sc[v]);
                 aw[i][v] = fma2(dp, f[i][v], aw[i][v]);
-                o[i][v] = mul2(dp, wp[v]);  // q
-                s2 = fma2(o[i][v], f[i][v], s2);
+                o[i][v] = mul2(rf1, fma2(f[i][v], mf, mul2(dp, wp[v])));
             }
             if (a.dr) norm_store<V>(a.dr, rb, base + c, dr[i]);
             if (a.dgate) norm_store<V>(a.dgate, xb, base + c, dg);
-        }
-        f32x2 mf = zero;
-        if (a.w_post) {
-            ss[0] = sum2(s2);
-            red.sum(ss);
-            mf = dup2(-(ss[0] * inv_d));
-        }
-        if (a.df) {
-#pragma unroll
-            for (int i = 0; i < P; ++i) {
-                const int c = at.col0 + (i * blockDim.x + threadIdx.x) * V;
-                if (c >= a.D) continue;
-#pragma unroll
-                for (int v = 0; v < N; ++v) o[i][v] = mul2(rf1, fma2(f[i][v], mf, o[i][v]));
-                norm_store<V>(a.df, fb, base + c, o[i]);
-            }
+            if (a.df) norm_store<V>(a.df, fb, base + c, o[i]);
         }
     }
     float* part = a.part + at.first * 3 * a.D;
