@@ -15,7 +15,9 @@ Typical use::
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
+import struct
 
 import torch
 
@@ -70,12 +72,6 @@ class Dims(ctypes.Structure):
 class _CState(ctypes.Structure):
     _fields_ = [("M", ctypes.c_void_p), ("stamp", ctypes.c_void_p), ("Lambda", ctypes.c_void_p),
                 ("M0", ctypes.c_void_p)]
-
-
-class _CView(ctypes.Structure):
-    """sdm_view"""
-    _fields_ = [("data", ctypes.c_void_p), ("sb", ctypes.c_int64), ("sh", ctypes.c_int64),
-                ("st", ctypes.c_int64)]
 
 
 class _ConvDims(ctypes.Structure):
@@ -135,7 +131,8 @@ def _load():
         "sdm_weight_stats_workspace_bytes": ([ctypes.c_int64, I32], SZ),
         "sdm_weight_stats": ([ctypes.c_int64, I32, P, P, P, P, I32, P, P, P, SZ, P], I32),
     }
-    V, CD, SD, ND = (ctypes.POINTER(c) for c in (_CView, _ConvDims, _ScanDims, _NormDims))
+    V = ctypes.c_char_p  # an sdm_view, packed
+    CD, SD, ND = (ctypes.POINTER(c) for c in (_ConvDims, _ScanDims, _NormDims))
     sig.update({
         "sdm_short_conv": ([CD, V, P, P, P, P, V, P], I32),
         "sdm_short_conv_backward_workspace_bytes": ([CD], SZ),
@@ -590,143 +587,183 @@ def layer_in(d: Dims, x: torch.Tensor, Win_t: torch.Tensor, A_log: torch.Tensor,
 # ---- the state-space block -------------------------------------------------------------------
 # Activations are taken as views (last dimension contiguous, other strides free); every tensor of
 # a call is on the same device, which need not be the current one.  With `stream` the call's own
-# buffers are allocated on that stream too.
+# buffers are allocated on that stream too.  A decode step calls these once a layer, so the checks
+# take one pass over each tensor and the dims structures are kept by their sizes.
+
+_pack_view = struct.Struct("=Qqqq").pack  # sdm_view
+
+
+def _refuse(t, what, shape, dtype, dev):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{what} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{what} is on {t.device}, the other inputs on cuda:{dev}")
+
 
 def _act_dtype(x, what):
     if not isinstance(x, torch.Tensor) or not x.is_cuda:
         raise TypeError(f"{what} must be a CUDA tensor")
-    if x.dtype not in _DT:
+    dt = _DT.get(x.dtype)
+    if dt is None:
         raise TypeError(f"{what} must be float32 or bfloat16, got {x.dtype}")
-    return _DT[x.dtype]
+    return dt
 
 
 def _arg(t, what, shape, dtype, dev):
     """Device address of an optional contiguous tensor of this shape, type and device."""
     if t is None:
         return None
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{what} must have shape {shape}, got {tuple(t.shape)}")
-    if t.device != dev:
-        raise ValueError(f"{what} is on {t.device}, the other inputs on {dev}")
-    return _ptr(t, what, dtype)
+    if type(t) is not torch.Tensor or t.dtype is not dtype or t.shape != shape or \
+            t.get_device() != dev:
+        _refuse(t, what, shape, dtype, dev)
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    return t.data_ptr()
 
 
-def _strided(t, what, shape, dtype, dev, axes):
-    """sdm_view of an activation: axes are its sequence, head (or -1) and token dimensions."""
+def _rows(t, what, shape, dtype, dev):
+    """sdm_view of a [sequence, token, column] activation, or None."""
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype:
-        raise TypeError(f"{what} must be a {dtype} tensor")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{what} must have shape {shape}, got {tuple(t.shape)}")
-    if t.device != dev:
-        raise ValueError(f"{what} is on {t.device}, the other inputs on {dev}")
-    st = t.stride()
-    if st[-1] != 1 and shape[-1] > 1:
+    if type(t) is not torch.Tensor or t.dtype is not dtype or t.shape != shape or \
+            t.get_device() != dev:
+        _refuse(t, what, shape, dtype, dev)
+    b, k, c = t.stride()
+    if c != 1 and shape[2] > 1:
         raise ValueError(f"{what}'s last dimension must be contiguous")
-    b, h, k = axes
-    return ctypes.byref(_CView(t.data_ptr(), st[b], st[h] if h >= 0 else 0, st[k]))
+    return _pack_view(t.data_ptr(), b, 0, k)
 
 
-class _On:
-    """The device and stream of a call: entered where they are not the current ones."""
-
-    def __init__(self, dev, stream):
-        self.ctx = None
-        if stream is not None:
-            if stream.device != dev:
-                raise ValueError(f"stream is on {stream.device}, the inputs on {dev}")
-            self.ctx = torch.cuda.stream(stream)
-        elif dev.index != torch.cuda.current_device():
-            self.ctx = torch.cuda.device(dev)
-
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+def _heads(t, what, shape, dtype, dev, token_first=False):
+    """sdm_view of a [sequence, head, token, column] activation (token_first: [sequence, token,
+    group, column])."""
+    if type(t) is not torch.Tensor or t.dtype is not dtype or t.shape != shape or \
+            t.get_device() != dev:
+        _refuse(t, what, shape, dtype, dev)
+    b, h, k, c = t.stride()
+    if c != 1 and shape[3] > 1:
+        raise ValueError(f"{what}'s last dimension must be contiguous")
+    return _pack_view(t.data_ptr(), b, k, h) if token_first else _pack_view(t.data_ptr(), b, h, k)
 
 
-def _new_rows(shape, dtype, dev, lens):
+def _on(dev, stream):
+    """A context where `stream` or the tensors' device is not the current one, else None."""
+    if stream is not None:
+        if stream.device.index != dev:
+            raise ValueError(f"stream is on {stream.device}, the inputs on cuda:{dev}")
+        return torch.cuda.stream(stream)
+    if dev != torch.cuda.current_device():
+        return torch.cuda.device(dev)
+    return None
+
+
+def _elsewhere(f):
+    """Runs f's calls on another stream or device than the current ones within its context."""
+    @functools.wraps(f)
+    def call(x, *args, stream=None, **kw):
+        if not isinstance(x, torch.Tensor) or not x.is_cuda:
+            raise TypeError(f"{f.__name__} takes CUDA tensors")
+        ctx = _on(x.get_device(), stream)
+        if ctx is None:
+            return f(x, *args, **kw)
+        with ctx:
+            return f(x, *args, **kw)
+    return call
+
+
+def _new_rows(like, lens):
     """A new output: zero behind the sequences of a padded batch, where nothing is written."""
     f = torch.empty if lens is None else torch.zeros
-    return f(shape, dtype=dtype, device=dev)
+    return f(like.shape, dtype=like.dtype, device=like.device)
 
 
-def _scratch(ws, nbytes, dev):
+def _scratch(ws, nbytes, like):
     if ws is None:
-        ws = torch.empty(max(16, nbytes), dtype=torch.uint8, device=dev)
-    elif ws.device != dev:
-        raise ValueError(f"ws is on {ws.device}, the inputs on {dev}")
+        ws = torch.empty(max(16, nbytes), dtype=torch.uint8, device=like.device)
+    elif ws.get_device() != like.get_device():
+        raise ValueError(f"ws is on {ws.device}, the inputs on {like.device}")
     return ws, _ptr(ws, "ws"), ws.numel() * ws.element_size()
 
 
 _ACT = {None: 0, "none": 0, "silu": 1}
 
 
+@functools.lru_cache(maxsize=1024)
+def _conv_dims(*sizes):
+    c = _ConvDims(*sizes)
+    return c, _lib.sdm_short_conv_backward_workspace_bytes(ctypes.byref(c))
+
+
 def _conv_setup(x, w, act, fresh):
     xdt = _act_dtype(x, "x")
     if x.dim() != 4 or not isinstance(w, torch.Tensor) or w.dim() != 3:
         raise ValueError("x must be [B, H, T, d] and w [H, d, K]")
-    B, H, T, d = x.shape
-    K = int(w.shape[2])
-    return _ConvDims(B, H, T, d, K, xdt, _ACT[act], 1 if fresh else 0)
+    if act not in _ACT:
+        raise ValueError(f"act must be None or 'silu', got {act!r}")
+    return _conv_dims(*x.shape, w.shape[2], xdt, _ACT[act], 1 if fresh else 0)
 
 
-def short_conv(x, w, bias=None, act="silu", state=None, lens=None, fresh=False, y=None,
-               stream=None):
+@_elsewhere
+def short_conv(x, w, bias=None, act="silu", state=None, lens=None, fresh=False, y=None):
     """sdm_short_conv: causal convolution of x [B,H,T,d] (fp32 or bf16; [B,T,D] as
     x.unsqueeze(1)) with w [H,d,K] fp32, bias [H,d] fp32 and act "silu" or None -> y like x.
     state [B,H,K-1,d] (x's type) holds the inputs before the call, oldest first, and is moved on in
     place (fresh=True: it is only written, the sequences start at zero).  lens [B] int32: tokens of
-    each sequence; y behind them is not written (zero in a new y)."""
-    c = _conv_setup(x, w, act, fresh)
-    dev, shape, ax = x.device, tuple(x.shape), (0, 1, 2)
-    with _On(dev, stream):
-        if y is None:
-            y = _new_rows(shape, x.dtype, dev, lens)
-        _ok(_lib.sdm_short_conv(
-            ctypes.byref(c), _strided(x, "x", shape, x.dtype, dev, ax),
-            _arg(w, "w", (c.H, c.d, c.K), torch.float32, dev),
-            _arg(bias, "bias", (c.H, c.d), torch.float32, dev),
-            _arg(state, "state", (c.B, c.H, c.K - 1, c.d), x.dtype, dev),
-            _arg(lens, "lens", (c.B,), torch.int32, dev),
-            _strided(y, "y", shape, x.dtype, dev, ax), _stream(stream)), "sdm_short_conv")
+    each sequence; y behind them is not written (zero in a new y).  Also takes stream=."""
+    c, _ = _conv_setup(x, w, act, fresh)
+    dev, shape, dt = x.get_device(), x.shape, x.dtype
+    B, H, T, d = shape
+    if y is None:
+        y = _new_rows(x, lens)
+    _ok(_lib.sdm_short_conv(
+        c, _heads(x, "x", shape, dt, dev), _arg(w, "w", (H, d, c.K), torch.float32, dev),
+        _arg(bias, "bias", (H, d), torch.float32, dev),
+        _arg(state, "state", (B, H, c.K - 1, d), dt, dev),
+        _arg(lens, "lens", (B,), torch.int32, dev), _heads(y, "y", shape, dt, dev), _stream()),
+        "sdm_short_conv")
     return y
 
 
+@_elsewhere
 def short_conv_backward(x, w, dy, bias=None, act="silu", state=None, lens=None, fresh=False,
-                        dstate_end=None, dx=None, ws=None, stream=None) -> dict:
+                        dstate_end=None, dx=None, ws=None) -> dict:
     """sdm_short_conv_backward: dict dx (x's type), dw, dbias and dstate (fp32; dbias with bias,
     dstate [B,H,K-1,d] with state) for dy like x and, optionally, the gradient dstate_end
-    [B,H,K-1,d] fp32 of the state after the call.  state: the state at the START of the call."""
-    c = _conv_setup(x, w, act, fresh)
-    dev, shape, ax = x.device, tuple(x.shape), (0, 1, 2)
-    st = (c.B, c.H, c.K - 1, c.d)
-    f = dict(dtype=torch.float32, device=dev)
-    with _On(dev, stream):
-        g = {"dx": torch.empty(shape, dtype=x.dtype, device=dev) if dx is None else dx,
-             "dw": torch.empty((c.H, c.d, c.K), **f)}
-        if bias is not None:
-            g["dbias"] = torch.empty((c.H, c.d), **f)
-        if state is not None:
-            g["dstate"] = torch.empty(st, **f)
-        ws, wp, wn = _scratch(ws, _lib.sdm_short_conv_backward_workspace_bytes(ctypes.byref(c)),
-                              dev)
-        _ok(_lib.sdm_short_conv_backward(
-            ctypes.byref(c), _strided(x, "x", shape, x.dtype, dev, ax),
-            _arg(w, "w", (c.H, c.d, c.K), torch.float32, dev),
-            _arg(bias, "bias", (c.H, c.d), torch.float32, dev),
-            _arg(state, "state", st, x.dtype, dev), _arg(lens, "lens", (c.B,), torch.int32, dev),
-            _strided(dy, "dy", shape, x.dtype, dev, ax),
-            _arg(dstate_end, "dstate_end", st, torch.float32, dev),
-            _strided(g["dx"], "dx", shape, x.dtype, dev, ax), g["dw"].data_ptr(),
-            g["dbias"].data_ptr() if bias is not None else None,
-            g["dstate"].data_ptr() if state is not None else None, wp, wn, _stream(stream)),
-            "sdm_short_conv_backward")
+    [B,H,K-1,d] fp32 of the state after the call.  state: the state at the START of the call.  Also
+    takes stream=."""
+    c, need = _conv_setup(x, w, act, fresh)
+    dev, shape, dt = x.get_device(), x.shape, x.dtype
+    B, H, T, d = shape
+    st = (B, H, c.K - 1, d)
+    f = dict(dtype=torch.float32, device=x.device)
+    g = {"dx": torch.empty(shape, dtype=dt, device=x.device) if dx is None else dx,
+         "dw": torch.empty((H, d, c.K), **f)}
+    if bias is not None:
+        g["dbias"] = torch.empty((H, d), **f)
+    if state is not None:
+        g["dstate"] = torch.empty(st, **f)
+    ws, wp, wn = _scratch(ws, need, x)
+    _ok(_lib.sdm_short_conv_backward(
+        c, _heads(x, "x", shape, dt, dev), _arg(w, "w", (H, d, c.K), torch.float32, dev),
+        _arg(bias, "bias", (H, d), torch.float32, dev), _arg(state, "state", st, dt, dev),
+        _arg(lens, "lens", (B,), torch.int32, dev), _heads(dy, "dy", shape, dt, dev),
+        _arg(dstate_end, "dstate_end", st, torch.float32, dev),
+        _heads(g["dx"], "dx", shape, dt, dev), g["dw"].data_ptr(),
+        g["dbias"].data_ptr() if bias is not None else None,
+        g["dstate"].data_ptr() if state is not None else None, wp, wn, _stream()),
+        "sdm_short_conv_backward")
     return g
+
+
+@functools.lru_cache(maxsize=1024)
+def _scan_dims(*sizes):
+    c = _ScanDims(*sizes)
+    return c, _lib.sdm_selective_scan_workspace_bytes(ctypes.byref(c)), \
+        _lib.sdm_selective_scan_backward_workspace_bytes(ctypes.byref(c))
 
 
 def _scan_setup(u, A, B, softplus, fresh):
@@ -734,153 +771,141 @@ def _scan_setup(u, A, B, softplus, fresh):
     if u.dim() != 3 or not isinstance(A, torch.Tensor) or A.dim() != 2 or \
             not isinstance(B, torch.Tensor) or B.dim() != 4:
         raise ValueError("u must be [B, T, D], A [D, N] and B [B, T, G, N]")
-    b, T, D = u.shape
-    return _ScanDims(b, T, D, int(A.shape[1]), int(B.shape[2]), xdt, 1 if softplus else 0,
-                     1 if fresh else 0)
+    return _scan_dims(*u.shape, A.shape[1], B.shape[2], xdt, 1 if softplus else 0,
+                      1 if fresh else 0)
 
 
 def _scan_inputs(c, u, delta, A, B, C, D, z, dt_bias, state, lens):
-    dev, dt = u.device, u.dtype
-    rows, ax = (c.B, c.T, c.D), (0, -1, 1)
-    gn, gax = (c.B, c.T, c.G, c.N), (0, 2, 1)
-    return (_strided(u, "u", rows, dt, dev, ax), _strided(delta, "delta", rows, dt, dev, ax),
-            _arg(A, "A", (c.D, c.N), torch.float32, dev), _strided(B, "B", gn, dt, dev, gax),
-            _strided(C, "C", gn, dt, dev, gax), _arg(D, "D", (c.D,), torch.float32, dev),
-            _strided(z, "z", rows, dt, dev, ax), _arg(dt_bias, "dt_bias", (c.D,), torch.float32, dev),
-            _arg(state, "state", (c.B, c.D, c.N), torch.float32, dev),
-            _arg(lens, "lens", (c.B,), torch.int32, dev))
+    dev, dt, rows, f32 = u.get_device(), u.dtype, u.shape, torch.float32
+    gn, ch = (c.B, c.T, c.G, c.N), (c.D,)
+    return (c, _rows(u, "u", rows, dt, dev), _rows(delta, "delta", rows, dt, dev),
+            _arg(A, "A", (c.D, c.N), f32, dev), _heads(B, "B", gn, dt, dev, True),
+            _heads(C, "C", gn, dt, dev, True), _arg(D, "D", ch, f32, dev),
+            _rows(z, "z", rows, dt, dev), _arg(dt_bias, "dt_bias", ch, f32, dev),
+            _arg(state, "state", (c.B, c.D, c.N), f32, dev), _arg(lens, "lens", (c.B,), torch.int32, dev))
 
 
+@_elsewhere
 def selective_scan(u, delta, A, B, C, D=None, z=None, dt_bias=None, state=None, lens=None,
-                   softplus=True, fresh=False, y=None, ws=None, stream=None):
+                   softplus=True, fresh=False, y=None, ws=None):
     """sdm_selective_scan: u, delta, z [B,T,D] and B, C [B,T,G,N] (fp32 or bf16), A [D,N], D and
     dt_bias [D] fp32 -> y like u.  state [B,D,N] fp32 is moved on in place (fresh=True: it is only
     written, the sequences start at zero); T = 1 is the decode step.  lens [B] int32: tokens of
-    each sequence; y behind them is not written (zero in a new y)."""
-    c = _scan_setup(u, A, B, softplus, fresh)
-    dev, rows = u.device, (c.B, c.T, c.D)
-    with _On(dev, stream):
-        if y is None:
-            y = _new_rows(rows, u.dtype, dev, lens)
-        need = _lib.sdm_selective_scan_workspace_bytes(ctypes.byref(c))
-        wp, wn = None, 0
-        if need or ws is not None:
-            ws, wp, wn = _scratch(ws, need, dev)
-        _ok(_lib.sdm_selective_scan(
-            ctypes.byref(c), *_scan_inputs(c, u, delta, A, B, C, D, z, dt_bias, state, lens),
-            _strided(y, "y", rows, u.dtype, dev, (0, -1, 1)), wp, wn, _stream(stream)),
-            "sdm_selective_scan")
+    each sequence; y behind them is not written (zero in a new y).  Also takes stream=."""
+    c, need, _ = _scan_setup(u, A, B, softplus, fresh)
+    inputs = _scan_inputs(c, u, delta, A, B, C, D, z, dt_bias, state, lens)
+    if y is None:
+        y = _new_rows(u, lens)
+    wp, wn = None, 0
+    if need or ws is not None:
+        ws, wp, wn = _scratch(ws, need, u)
+    _ok(_lib.sdm_selective_scan(*inputs, _rows(y, "y", u.shape, u.dtype, u.get_device()), wp, wn,
+                                _stream()), "sdm_selective_scan")
     return y
 
 
+@_elsewhere
 def selective_scan_backward(u, delta, A, B, C, dy, D=None, z=None, dt_bias=None, state=None,
-                            lens=None, softplus=True, fresh=False, dstate_end=None, ws=None,
-                            stream=None) -> dict:
+                            lens=None, softplus=True, fresh=False, dstate_end=None, ws=None) -> dict:
     """sdm_selective_scan_backward: dict du, ddelta, dB, dC and (with z) dz in u's type; dA and,
     with their inputs, dD, ddt_bias and dstate [B,D,N] in fp32, for dy like u and, optionally, the
     gradient dstate_end [B,D,N] fp32 of the state after the call.  state: the state at the START of
-    the call."""
-    c = _scan_setup(u, A, B, softplus, fresh)
-    dev, dt = u.device, u.dtype
-    rows, gn, st, ax = (c.B, c.T, c.D), (c.B, c.T, c.G, c.N), (c.B, c.D, c.N), (0, -1, 1)
-    with _On(dev, stream):
-        def new(shape, dtype):
-            return torch.empty(shape, dtype=dtype, device=dev)
-        g = {"du": new(rows, dt), "ddelta": new(rows, dt), "dA": new((c.D, c.N), torch.float32),
-             "dB": new(gn, dt), "dC": new(gn, dt)}
-        if D is not None:
-            g["dD"] = new((c.D,), torch.float32)
-        if z is not None:
-            g["dz"] = new(rows, dt)
-        if dt_bias is not None:
-            g["ddt_bias"] = new((c.D,), torch.float32)
-        if state is not None:
-            g["dstate"] = new(st, torch.float32)
-        ws, wp, wn = _scratch(
-            ws, _lib.sdm_selective_scan_backward_workspace_bytes(ctypes.byref(c)), dev)
+    the call.  Also takes stream=."""
+    c, _, need = _scan_setup(u, A, B, softplus, fresh)
+    inputs = _scan_inputs(c, u, delta, A, B, C, D, z, dt_bias, state, lens)
+    dev, dt, rows, f32 = u.get_device(), u.dtype, u.shape, torch.float32
+    gn, st = (c.B, c.T, c.G, c.N), (c.B, c.D, c.N)
 
-        def p(name):
-            return g[name].data_ptr() if name in g else None
-        _ok(_lib.sdm_selective_scan_backward(
-            ctypes.byref(c), *_scan_inputs(c, u, delta, A, B, C, D, z, dt_bias, state, lens),
-            _strided(dy, "dy", rows, dt, dev, ax),
-            _arg(dstate_end, "dstate_end", st, torch.float32, dev),
-            _strided(g["du"], "du", rows, dt, dev, ax),
-            _strided(g["ddelta"], "ddelta", rows, dt, dev, ax), p("dA"), p("dB"), p("dC"),
-            p("dD"), _strided(g.get("dz"), "dz", rows, dt, dev, ax), p("ddt_bias"), p("dstate"),
-            wp, wn, _stream(stream)), "sdm_selective_scan_backward")
+    def new(shape, dtype):
+        return torch.empty(shape, dtype=dtype, device=u.device)
+    g = {"du": new(rows, dt), "ddelta": new(rows, dt), "dA": new((c.D, c.N), f32),
+         "dB": new(gn, dt), "dC": new(gn, dt)}
+    if D is not None:
+        g["dD"] = new((c.D,), f32)
+    if z is not None:
+        g["dz"] = new(rows, dt)
+    if dt_bias is not None:
+        g["ddt_bias"] = new((c.D,), f32)
+    if state is not None:
+        g["dstate"] = new(st, f32)
+    ws, wp, wn = _scratch(ws, need, u)
+
+    def p(name):
+        return g[name].data_ptr() if name in g else None
+    _ok(_lib.sdm_selective_scan_backward(
+        *inputs, _rows(dy, "dy", rows, dt, dev), _arg(dstate_end, "dstate_end", st, f32, dev),
+        _rows(g["du"], "du", rows, dt, dev), _rows(g["ddelta"], "ddelta", rows, dt, dev), p("dA"),
+        p("dB"), p("dC"), p("dD"), _rows(g.get("dz"), "dz", rows, dt, dev), p("ddt_bias"),
+        p("dstate"), wp, wn, _stream()), "sdm_selective_scan_backward")
     return g
+
+
+@functools.lru_cache(maxsize=1024)
+def _norm_dims(*sizes):
+    c = _NormDims(*sizes)
+    return c, _lib.sdm_block_norm_backward_workspace_bytes(ctypes.byref(c))
 
 
 def _norm_setup(r, f, x_dtype, eps):
     rdt, fdt = _act_dtype(r, "r"), _act_dtype(f, "f")
+    if x_dtype not in _DT:
+        raise TypeError(f"gate, n and dn are float32 or bfloat16, got {x_dtype}")
     D = int(r.shape[-1]) if r.dim() else 0
-    rows = r.numel() // D if D else 0
-    return _NormDims(rows, D, rdt, fdt, _DT[x_dtype], float(eps))
+    return _norm_dims(r.numel() // D if D else 0, D, rdt, fdt, _DT[x_dtype], float(eps))
 
 
+@_elsewhere
 def block_norm(r, f, w_post=None, gate=None, scale=None, w_pre=None, eps: float = 1e-6,
-               x_dtype=None, r_out=None, n=None, stream=None):
+               x_dtype=None, r_out=None, n=None):
     """sdm_block_norm: o = r + scale * sigmoid(gate) * rmsnorm(f) * w_post and n = rmsnorm(o) *
     w_pre over the last dimension of r, f, gate [..., D] -> (r_out like r, n).  r and f are fp32 or
     bf16 each; n has gate's type, or x_dtype (default bfloat16) without a gate.  w_post None: f
-    is not normalised.  r_out may be r."""
+    is not normalised.  r_out may be r.  Also takes stream=."""
     xdt = gate.dtype if gate is not None else (x_dtype or torch.bfloat16)
-    if xdt not in _DT:
-        raise TypeError(f"gate must be float32 or bfloat16, got {xdt}")
-    c = _norm_setup(r, f, xdt, eps)
-    dev, shape = r.device, tuple(r.shape)
-    with _On(dev, stream):
-        if r_out is None:
-            r_out = torch.empty(shape, dtype=r.dtype, device=dev)
-        if n is None:
-            n = torch.empty(shape, dtype=xdt, device=dev)
-        if c.rows > 0:
-            _ok(_lib.sdm_block_norm(
-                ctypes.byref(c), _arg(r, "r", shape, r.dtype, dev),
-                _arg(f, "f", shape, f.dtype, dev),
-                _arg(w_post, "w_post", (c.D,), torch.float32, dev),
-                _arg(gate, "gate", shape, xdt, dev),
-                _arg(scale, "scale", (c.D,), torch.float32, dev),
-                _arg(w_pre, "w_pre", (c.D,), torch.float32, dev),
-                _arg(r_out, "r_out", shape, r.dtype, dev), _arg(n, "n", shape, xdt, dev),
-                _stream(stream)), "sdm_block_norm")
+    c, _ = _norm_setup(r, f, xdt, eps)
+    dev, shape, col, f32 = r.get_device(), r.shape, (c.D,), torch.float32
+    if r_out is None:
+        r_out = torch.empty(shape, dtype=r.dtype, device=r.device)
+    if n is None:
+        n = torch.empty(shape, dtype=xdt, device=r.device)
+    args = (c, _arg(r, "r", shape, r.dtype, dev), _arg(f, "f", shape, f.dtype, dev),
+            _arg(w_post, "w_post", col, f32, dev), _arg(gate, "gate", shape, xdt, dev),
+            _arg(scale, "scale", col, f32, dev), _arg(w_pre, "w_pre", col, f32, dev),
+            _arg(r_out, "r_out", shape, r.dtype, dev), _arg(n, "n", shape, xdt, dev), _stream())
+    if c.rows > 0:
+        _ok(_lib.sdm_block_norm(*args), "sdm_block_norm")
     return r_out, n
 
 
+@_elsewhere
 def block_norm_backward(r, f, dr_out, dn, w_post=None, gate=None, scale=None, w_pre=None,
-                        eps: float = 1e-6, ws=None, stream=None) -> dict:
+                        eps: float = 1e-6, ws=None) -> dict:
     """sdm_block_norm_backward: dict dr, df, and with their inputs dgate, dscale, dw_post, dw_pre
     (sums in fp32, the others in their input's type) for the gradients dr_out (r's type) and dn
-    (gate's type) of block_norm's outputs; either may be None (zero)."""
+    (gate's type) of block_norm's outputs; either may be None (zero).  Also takes stream=."""
     if dr_out is None and dn is None:
         raise ValueError("dr_out or dn is needed")
     xdt = gate.dtype if gate is not None else (dn.dtype if dn is not None else torch.bfloat16)
-    if xdt not in _DT:
-        raise TypeError(f"gate and dn must be float32 or bfloat16, got {xdt}")
-    c = _norm_setup(r, f, xdt, eps)
-    dev, shape = r.device, tuple(r.shape)
-    with _On(dev, stream):
-        g = {"dr": torch.empty(shape, dtype=r.dtype, device=dev),
-             "df": torch.empty(shape, dtype=f.dtype, device=dev)}
-        if gate is not None:
-            g["dgate"] = torch.empty(shape, dtype=xdt, device=dev)
-        for name, w in (("dscale", scale), ("dw_post", w_post), ("dw_pre", w_pre)):
-            if w is not None:
-                g[name] = torch.empty((c.D,), dtype=torch.float32, device=dev)
+    c, need = _norm_setup(r, f, xdt, eps)
+    dev, shape, col, f32 = r.get_device(), r.shape, (c.D,), torch.float32
+    g = {"dr": torch.empty(shape, dtype=r.dtype, device=r.device),
+         "df": torch.empty(shape, dtype=f.dtype, device=r.device)}
+    if gate is not None:
+        g["dgate"] = torch.empty(shape, dtype=xdt, device=r.device)
+    for name, w in (("dscale", scale), ("dw_post", w_post), ("dw_pre", w_pre)):
+        if w is not None:
+            g[name] = torch.empty(col, dtype=f32, device=r.device)
 
-        def p(name):
-            return g[name].data_ptr() if name in g else None
-        if c.D == 0:
-            return g
-        ws, wp, wn = _scratch(ws, _lib.sdm_block_norm_backward_workspace_bytes(ctypes.byref(c)),
-                              dev)
-        _ok(_lib.sdm_block_norm_backward(
-            ctypes.byref(c), _arg(r, "r", shape, r.dtype, dev), _arg(f, "f", shape, f.dtype, dev),
-            _arg(w_post, "w_post", (c.D,), torch.float32, dev),
-            _arg(gate, "gate", shape, xdt, dev), _arg(scale, "scale", (c.D,), torch.float32, dev),
-            _arg(w_pre, "w_pre", (c.D,), torch.float32, dev),
-            _arg(dr_out, "dr_out", shape, r.dtype, dev), _arg(dn, "dn", shape, xdt, dev),
-            p("dr"), p("df"), p("dgate"), p("dscale"), p("dw_post"), p("dw_pre"), wp, wn,
-            _stream(stream)), "sdm_block_norm_backward")
+    def p(name):
+        return g[name].data_ptr() if name in g else None
+    if c.D == 0:
+        return g
+    ws, wp, wn = _scratch(ws, need, r)
+    _ok(_lib.sdm_block_norm_backward(
+        c, _arg(r, "r", shape, r.dtype, dev), _arg(f, "f", shape, f.dtype, dev),
+        _arg(w_post, "w_post", col, f32, dev), _arg(gate, "gate", shape, xdt, dev),
+        _arg(scale, "scale", col, f32, dev), _arg(w_pre, "w_pre", col, f32, dev),
+        _arg(dr_out, "dr_out", shape, r.dtype, dev), _arg(dn, "dn", shape, xdt, dev),
+        p("dr"), p("df"), p("dgate"), p("dscale"), p("dw_post"), p("dw_pre"), wp, wn, _stream()),
+        "sdm_block_norm_backward")
     return g
