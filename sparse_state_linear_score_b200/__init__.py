@@ -650,35 +650,29 @@ def _heads(t, what, shape, dtype, dev, token_first=False):
     return _pack_view(t.data_ptr(), b, k, h) if token_first else _pack_view(t.data_ptr(), b, h, k)
 
 
-def _on(dev, stream):
-    """A context where `stream` or the tensors' device is not the current one, else None."""
-    if stream is not None:
-        if stream.device.index != dev:
-            raise ValueError(f"stream is on {stream.device}, the inputs on cuda:{dev}")
-        return torch.cuda.stream(stream)
-    if dev != torch.cuda.current_device():
-        return torch.cuda.device(dev)
-    return None
+_here = _cur_device or torch.cuda.current_device
 
 
-def _elsewhere(f):
-    """Runs f's calls on another stream or device than the current ones within its context."""
-    @functools.wraps(f)
-    def call(x, *args, stream=None, **kw):
-        if not isinstance(x, torch.Tensor) or not x.is_cuda:
-            raise TypeError(f"{f.__name__} takes CUDA tensors")
-        ctx = _on(x.get_device(), stream)
-        if ctx is None:
-            return f(x, *args, **kw)
-        with ctx:
-            return f(x, *args, **kw)
-    return call
+def _elsewhere(f, stream, x, *args):
+    """f on another stream or device than the current ones: within its context."""
+    if not isinstance(x, torch.Tensor) or not x.is_cuda:
+        raise TypeError(f"{f.__name__} takes CUDA tensors")
+    if stream is not None and stream.device != x.device:
+        raise ValueError(f"stream is on {stream.device}, the inputs on {x.device}")
+    with torch.cuda.device(x.device) if stream is None else torch.cuda.stream(stream):
+        return f(x, *args)
 
 
 def _new_rows(like, lens):
     """A new output: zero behind the sequences of a padded batch, where nothing is written."""
-    f = torch.empty if lens is None else torch.zeros
-    return f(like.shape, dtype=like.dtype, device=like.device)
+    if lens is None:
+        return _new_like(like)
+    return torch.zeros(like.shape, dtype=like.dtype, device=like.device)
+
+
+def _new_like(t):
+    return torch.empty_like(t) if t.is_contiguous() else \
+        torch.empty(t.shape, dtype=t.dtype, device=t.device)
 
 
 def _scratch(ws, nbytes, like):
@@ -704,51 +698,56 @@ def _conv_setup(x, w, act, fresh):
         raise ValueError("x must be [B, H, T, d] and w [H, d, K]")
     if act not in _ACT:
         raise ValueError(f"act must be None or 'silu', got {act!r}")
-    return _conv_dims(*x.shape, w.shape[2], xdt, _ACT[act], 1 if fresh else 0)
+    K = w.shape[2]
+    return _conv_dims(*x.shape, K, xdt, _ACT[act], 1 if fresh else 0), K
 
 
-@_elsewhere
-def short_conv(x, w, bias=None, act="silu", state=None, lens=None, fresh=False, y=None):
+def short_conv(x, w, bias=None, act="silu", state=None, lens=None, fresh=False, y=None,
+               stream=None):
     """sdm_short_conv: causal convolution of x [B,H,T,d] (fp32 or bf16; [B,T,D] as
     x.unsqueeze(1)) with w [H,d,K] fp32, bias [H,d] fp32 and act "silu" or None -> y like x.
     state [B,H,K-1,d] (x's type) holds the inputs before the call, oldest first, and is moved on in
     place (fresh=True: it is only written, the sequences start at zero).  lens [B] int32: tokens of
-    each sequence; y behind them is not written (zero in a new y).  Also takes stream=."""
-    c, _ = _conv_setup(x, w, act, fresh)
+    each sequence; y behind them is not written (zero in a new y)."""
+    if stream is not None or not isinstance(x, torch.Tensor) or x.get_device() != _here():
+        return _elsewhere(short_conv, stream, x, w, bias, act, state, lens, fresh, y)
+    (c, _), K = _conv_setup(x, w, act, fresh)
     dev, shape, dt = x.get_device(), x.shape, x.dtype
     B, H, T, d = shape
     if y is None:
         y = _new_rows(x, lens)
     _ok(_lib.sdm_short_conv(
-        c, _heads(x, "x", shape, dt, dev), _arg(w, "w", (H, d, c.K), torch.float32, dev),
+        c, _heads(x, "x", shape, dt, dev), _arg(w, "w", (H, d, K), torch.float32, dev),
         _arg(bias, "bias", (H, d), torch.float32, dev),
-        _arg(state, "state", (B, H, c.K - 1, d), dt, dev),
+        _arg(state, "state", (B, H, K - 1, d), dt, dev),
         _arg(lens, "lens", (B,), torch.int32, dev), _heads(y, "y", shape, dt, dev), _stream()),
         "sdm_short_conv")
     return y
 
 
-@_elsewhere
 def short_conv_backward(x, w, dy, bias=None, act="silu", state=None, lens=None, fresh=False,
-                        dstate_end=None, dx=None, ws=None) -> dict:
+                        dstate_end=None, dx=None, ws=None,
+                        stream=None) -> dict:
     """sdm_short_conv_backward: dict dx (x's type), dw, dbias and dstate (fp32; dbias with bias,
     dstate [B,H,K-1,d] with state) for dy like x and, optionally, the gradient dstate_end
-    [B,H,K-1,d] fp32 of the state after the call.  state: the state at the START of the call.  Also
-    takes stream=."""
-    c, need = _conv_setup(x, w, act, fresh)
+    [B,H,K-1,d] fp32 of the state after the call.  state: the state at the START of the call."""
+    if stream is not None or not isinstance(x, torch.Tensor) or x.get_device() != _here():
+        return _elsewhere(short_conv_backward, stream, x, w, dy, bias, act, state, lens, fresh,
+                          dstate_end, dx, ws)
+    (c, need), K = _conv_setup(x, w, act, fresh)
     dev, shape, dt = x.get_device(), x.shape, x.dtype
     B, H, T, d = shape
-    st = (B, H, c.K - 1, d)
+    st = (B, H, K - 1, d)
     f = dict(dtype=torch.float32, device=x.device)
-    g = {"dx": torch.empty(shape, dtype=dt, device=x.device) if dx is None else dx,
-         "dw": torch.empty((H, d, c.K), **f)}
+    g = {"dx": _new_like(x) if dx is None else dx,
+         "dw": torch.empty((H, d, K), **f)}
     if bias is not None:
         g["dbias"] = torch.empty((H, d), **f)
     if state is not None:
         g["dstate"] = torch.empty(st, **f)
     ws, wp, wn = _scratch(ws, need, x)
     _ok(_lib.sdm_short_conv_backward(
-        c, _heads(x, "x", shape, dt, dev), _arg(w, "w", (H, d, c.K), torch.float32, dev),
+        c, _heads(x, "x", shape, dt, dev), _arg(w, "w", (H, d, K), torch.float32, dev),
         _arg(bias, "bias", (H, d), torch.float32, dev), _arg(state, "state", st, dt, dev),
         _arg(lens, "lens", (B,), torch.int32, dev), _heads(dy, "dy", shape, dt, dev),
         _arg(dstate_end, "dstate_end", st, torch.float32, dev),
@@ -777,21 +776,25 @@ def _scan_setup(u, A, B, softplus, fresh):
 
 def _scan_inputs(c, u, delta, A, B, C, D, z, dt_bias, state, lens):
     dev, dt, rows, f32 = u.get_device(), u.dtype, u.shape, torch.float32
-    gn, ch = (c.B, c.T, c.G, c.N), (c.D,)
+    (b, T, Dn), N = rows, A.shape[1]
+    gn, ch = (b, T, B.shape[2], N), (Dn,)
     return (c, _rows(u, "u", rows, dt, dev), _rows(delta, "delta", rows, dt, dev),
-            _arg(A, "A", (c.D, c.N), f32, dev), _heads(B, "B", gn, dt, dev, True),
+            _arg(A, "A", (Dn, N), f32, dev), _heads(B, "B", gn, dt, dev, True),
             _heads(C, "C", gn, dt, dev, True), _arg(D, "D", ch, f32, dev),
             _rows(z, "z", rows, dt, dev), _arg(dt_bias, "dt_bias", ch, f32, dev),
-            _arg(state, "state", (c.B, c.D, c.N), f32, dev), _arg(lens, "lens", (c.B,), torch.int32, dev))
+            _arg(state, "state", (b, Dn, N), f32, dev), _arg(lens, "lens", (b,), torch.int32, dev))
 
 
-@_elsewhere
 def selective_scan(u, delta, A, B, C, D=None, z=None, dt_bias=None, state=None, lens=None,
-                   softplus=True, fresh=False, y=None, ws=None):
+                   softplus=True, fresh=False, y=None, ws=None,
+                   stream=None):
     """sdm_selective_scan: u, delta, z [B,T,D] and B, C [B,T,G,N] (fp32 or bf16), A [D,N], D and
     dt_bias [D] fp32 -> y like u.  state [B,D,N] fp32 is moved on in place (fresh=True: it is only
     written, the sequences start at zero); T = 1 is the decode step.  lens [B] int32: tokens of
-    each sequence; y behind them is not written (zero in a new y).  Also takes stream=."""
+    each sequence; y behind them is not written (zero in a new y)."""
+    if stream is not None or not isinstance(u, torch.Tensor) or u.get_device() != _here():
+        return _elsewhere(selective_scan, stream, u, delta, A, B, C, D, z, dt_bias, state, lens,
+                          softplus, fresh, y, ws)
     c, need, _ = _scan_setup(u, A, B, softplus, fresh)
     inputs = _scan_inputs(c, u, delta, A, B, C, D, z, dt_bias, state, lens)
     if y is None:
@@ -804,13 +807,16 @@ def selective_scan(u, delta, A, B, C, D=None, z=None, dt_bias=None, state=None, 
     return y
 
 
-@_elsewhere
 def selective_scan_backward(u, delta, A, B, C, dy, D=None, z=None, dt_bias=None, state=None,
-                            lens=None, softplus=True, fresh=False, dstate_end=None, ws=None) -> dict:
+                            lens=None, softplus=True, fresh=False, dstate_end=None, ws=None,
+                            stream=None) -> dict:
     """sdm_selective_scan_backward: dict du, ddelta, dB, dC and (with z) dz in u's type; dA and,
     with their inputs, dD, ddt_bias and dstate [B,D,N] in fp32, for dy like u and, optionally, the
     gradient dstate_end [B,D,N] fp32 of the state after the call.  state: the state at the START of
-    the call.  Also takes stream=."""
+    the call."""
+    if stream is not None or not isinstance(u, torch.Tensor) or u.get_device() != _here():
+        return _elsewhere(selective_scan_backward, stream, u, delta, A, B, C, dy, D, z, dt_bias,
+                          state, lens, softplus, fresh, dstate_end, ws)
     c, _, need = _scan_setup(u, A, B, softplus, fresh)
     inputs = _scan_inputs(c, u, delta, A, B, C, D, z, dt_bias, state, lens)
     dev, dt, rows, f32 = u.get_device(), u.dtype, u.shape, torch.float32
@@ -854,20 +860,25 @@ def _norm_setup(r, f, x_dtype, eps):
     return _norm_dims(r.numel() // D if D else 0, D, rdt, fdt, _DT[x_dtype], float(eps))
 
 
-@_elsewhere
 def block_norm(r, f, w_post=None, gate=None, scale=None, w_pre=None, eps: float = 1e-6,
-               x_dtype=None, r_out=None, n=None):
+               x_dtype=None, r_out=None, n=None,
+               stream=None):
     """sdm_block_norm: o = r + scale * sigmoid(gate) * rmsnorm(f) * w_post and n = rmsnorm(o) *
     w_pre over the last dimension of r, f, gate [..., D] -> (r_out like r, n).  r and f are fp32 or
     bf16 each; n has gate's type, or x_dtype (default bfloat16) without a gate.  w_post None: f
-    is not normalised.  r_out may be r.  Also takes stream=."""
+    is not normalised.  r_out may be r."""
+    if stream is not None or not isinstance(r, torch.Tensor) or r.get_device() != _here():
+        return _elsewhere(block_norm, stream, r, f, w_post, gate, scale, w_pre, eps, x_dtype,
+                          r_out, n)
     xdt = gate.dtype if gate is not None else (x_dtype or torch.bfloat16)
     c, _ = _norm_setup(r, f, xdt, eps)
-    dev, shape, col, f32 = r.get_device(), r.shape, (c.D,), torch.float32
+    dev, shape, f32 = r.get_device(), r.shape, torch.float32
+    col = shape[-1:]
     if r_out is None:
-        r_out = torch.empty(shape, dtype=r.dtype, device=r.device)
+        r_out = _new_like(r)
     if n is None:
-        n = torch.empty(shape, dtype=xdt, device=r.device)
+        n = _new_like(gate) if gate is not None else \
+            torch.empty(shape, dtype=xdt, device=r.device)
     args = (c, _arg(r, "r", shape, r.dtype, dev), _arg(f, "f", shape, f.dtype, dev),
             _arg(w_post, "w_post", col, f32, dev), _arg(gate, "gate", shape, xdt, dev),
             _arg(scale, "scale", col, f32, dev), _arg(w_pre, "w_pre", col, f32, dev),
@@ -877,21 +888,24 @@ def block_norm(r, f, w_post=None, gate=None, scale=None, w_pre=None, eps: float 
     return r_out, n
 
 
-@_elsewhere
 def block_norm_backward(r, f, dr_out, dn, w_post=None, gate=None, scale=None, w_pre=None,
-                        eps: float = 1e-6, ws=None) -> dict:
+                        eps: float = 1e-6, ws=None,
+                        stream=None) -> dict:
     """sdm_block_norm_backward: dict dr, df, and with their inputs dgate, dscale, dw_post, dw_pre
     (sums in fp32, the others in their input's type) for the gradients dr_out (r's type) and dn
-    (gate's type) of block_norm's outputs; either may be None (zero).  Also takes stream=."""
+    (gate's type) of block_norm's outputs; either may be None (zero)."""
+    if stream is not None or not isinstance(r, torch.Tensor) or r.get_device() != _here():
+        return _elsewhere(block_norm_backward, stream, r, f, dr_out, dn, w_post, gate, scale,
+                          w_pre, eps, ws)
     if dr_out is None and dn is None:
         raise ValueError("dr_out or dn is needed")
     xdt = gate.dtype if gate is not None else (dn.dtype if dn is not None else torch.bfloat16)
     c, need = _norm_setup(r, f, xdt, eps)
-    dev, shape, col, f32 = r.get_device(), r.shape, (c.D,), torch.float32
-    g = {"dr": torch.empty(shape, dtype=r.dtype, device=r.device),
-         "df": torch.empty(shape, dtype=f.dtype, device=r.device)}
+    dev, shape, f32 = r.get_device(), r.shape, torch.float32
+    col = shape[-1:]
+    g = {"dr": _new_like(r), "df": _new_like(f)}
     if gate is not None:
-        g["dgate"] = torch.empty(shape, dtype=xdt, device=r.device)
+        g["dgate"] = _new_like(gate)
     for name, w in (("dscale", scale), ("dw_post", w_post), ("dw_pre", w_pre)):
         if w is not None:
             g[name] = torch.empty(col, dtype=f32, device=r.device)
