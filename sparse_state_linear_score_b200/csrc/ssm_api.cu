@@ -354,11 +354,11 @@ ScanBwdPlan scan_bwd_plan(const sdm_scan_dims* d) {
     ScanBwdPlan p{};
     p.NN = pad_states(d->N);
     p.nchunk = (int)std::max(1LL, ceil_div(d->T, BWD_CHUNK));
-    const int ch = BWD_THREADS / (p.NN / 4), all = (int)ceil_div(d->D / d->G, ch);
-    // channel tiles of a block: more tiles, fewer shares of dB and dC to write and add; as many
-    // as leave four blocks an SM
+    // a block's channels by turns of its warps: more turns, fewer shares of dB and dC to write and
+    // add; as many as leave six blocks an SM, two for each of the three that fit
+    const int ch = BWD_WARPS * 32 / (p.NN / 4), all = (int)ceil_div(d->D / d->G, ch);
     const long long rest = (long long)d->B * p.nchunk * d->G;
-    const long long want = std::max(1LL, std::min<long long>(all, ceil_div(4 * kSms, rest)));
+    const long long want = std::max(1LL, std::min<long long>(all, ceil_div(6 * kSms, rest)));
     p.tiles = (int)ceil_div(all, want);
     p.blocks = (int)ceil_div(all, p.tiles);
     const size_t bk = (size_t)d->B * p.nchunk, states = bk * d->D * d->N * 4;
@@ -388,10 +388,12 @@ sdm_status launch_scan_bwd_t(const ScanBwdArgs<T>& A, const ScanBwdPlan& p,
         scan_carry_kernel<T><<<n, 256, 0, s>>>(a, 0);
         scan_carry_kernel<T><<<n, 256, 0, s>>>(a, 1);
     }
-    const size_t smem = bwd_smem(NN);
+    ScanBwdArgs<T> B = A;
+    set_pieces(B.s, v, 32 / LN, NN);
+    constexpr size_t smem = sizeof(BwdShared<T, LN>);
     if (!allow_smem(scan_bwd_kernel<T, LN>, smem)) return SDM_ERR_CUDA;
     scan_bwd_kernel<T, LN>
-        <<<dim3((unsigned)(a.G * p.blocks), p.nchunk, a.B), BWD_THREADS, smem, s>>>(A);
+        <<<dim3((unsigned)(a.G * p.blocks), p.nchunk, a.B), BWD_WARPS * 32, smem, s>>>(B);
     return launched();
 }
 
