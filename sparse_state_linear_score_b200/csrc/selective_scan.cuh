@@ -51,6 +51,7 @@ struct ScanArgs {
     const float* dstate_end;
     int B, T_, D, N, G, softplus, fresh;
     int chunk, nchunk;  // tokens of a chunk
+    int run;            // tokens of a walk: its chunk, or (SCAN_CHUNK_REV) several
 };
 
 // Sums v[i], i < 8, over LN neighbouring lanes; lane l of them ends with token k*LN + l in v[k].
@@ -271,7 +272,7 @@ __global__ void __launch_bounds__(32, NPT <= 4 ? 12 : 8) scan_walk_kernel(ScanAr
     const ScanLane<NPT, LN> L(a.D, a.G);
     const int lane = threadIdx.x;
     const int len = clamp_len(a.lens, L.b, a.T_);
-    const int t0 = blockIdx.y * a.chunk, t1 = min(t0 + a.chunk, len);
+    const int t0 = blockIdx.y * a.run, t1 = min(t0 + a.run, len);
     if (OUT && t0 >= len && blockIdx.y > 0) return;
     const bool gate = a.z.v.p && (OUT || REV);
     RowCopy<T, WCH, SCAN_TILE> cu, cd, cz, cg;
@@ -324,7 +325,7 @@ __global__ void __launch_bounds__(32, NPT <= 4 ? 12 : 8) scan_walk_kernel(ScanAr
     const f32x2 skip = OUT && a.Dskip ? pack2(a.Dskip[i0], a.Dskip[i1]) : dup2(0.f);
     T* yp = OUT ? a.y.p + L.b * a.y.sb + L.c0 + ic : nullptr;
     const bool pair = OUT && ic + 1 < L.cols && ((uintptr_t)yp % (2 * sizeof(T))) == 0 && a.y.st % 2 == 0;
-    f32x2 steps = dup2(0.f);
+    f32x2 steps = dup2(0.f), ahead = dup2(0.f);  // of the chunk so far, of the next tile
     const unsigned long long m_sp = a.softplus ? ~0ull : 0ull, m_z = gate ? ~0ull : 0ull;
     const float2* tok = sh.tok + lane / LN;
 
@@ -332,6 +333,10 @@ __global__ void __launch_bounds__(32, NPT <= 4 ? 12 : 8) scan_walk_kernel(ScanAr
     f32x2 st2[PAIRS], su2[PAIRS], g2[PAIRS];
     auto tile_steps = [&](int tile) {
         const auto& s = sh.st[tile % SCAN_STAGES];
+        if (!OUT) {
+            steps = add2(steps, ahead);
+            ahead = dup2(0.f);
+        }
 #pragma unroll
         for (int k = 0; k < PAIRS; ++k) {
             const int e = 2 * (lane + 32 * k);
@@ -345,7 +350,7 @@ __global__ void __launch_bounds__(32, NPT <= 4 ? 12 : 8) scan_walk_kernel(ScanAr
             st2[k] = (sp & m_sp) | (st2[k] & ~m_sp);
             st2[k] &= t0 + tile * SCAN_TILE + e / WCH < t1 ? ~0ull : 0ull;  // else the state stays
             su2[k] = mul2(st2[k], pack2(u[0], u[1]));
-            if (!OUT) steps = add2(steps, st2[k]);
+            if (!OUT) ahead = add2(ahead, st2[k]);
             if (REV) {
                 g2[k] = pack2(g[0], g[1]);
                 const f32x2 gz = mul2(g2[k], silu2(pack2(z[0], z[1])));
@@ -427,6 +432,38 @@ __global__ void __launch_bounds__(32, NPT <= 4 ? 12 : 8) scan_walk_kernel(ScanAr
         }
     };
 
+    // what a chunk leaves; the next starts from zero
+    auto emit = [&](int chunk) {
+        const long long to = ((long long)L.b * a.nchunk + chunk) * a.D + L.c;
+        float v[NPT];
+#pragma unroll
+        for (int i = 0; i < NP; ++i) unpack2(h[i], v[2 * i], v[2 * i + 1]);
+        L.store(a.E + to * a.N, a.N, v);
+        if (REV) {
+#pragma unroll
+            for (int i = 0; i < NP; ++i) unpack2(r[i], v[2 * i], v[2 * i + 1]);
+            L.store(a.R + to * a.N, a.N, v);
+        }
+        float s0, s1;
+        unpack2(steps, s0, s1);
+#pragma unroll
+        for (int m = WCH / 2; m < 32; m <<= 1) {
+            s0 += __shfl_xor_sync(0xffffffffu, s0, m);
+            s1 += __shfl_xor_sync(0xffffffffu, s1, m);
+        }
+        if (lane < WCH / 2) {
+            float* S = a.S + ((long long)L.b * a.nchunk + chunk) * a.D + L.c0;
+            if (ic < L.cols) S[ic] = s0;
+            if (ic + 1 < L.cols) S[ic + 1] = s1;
+        }
+        steps = dup2(0.f);
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            h[i] = r[i] = dup2(0.f);
+            P[i] = dup2(1.f);
+        }
+    };
+
     const int tiles = max(0, (t1 - t0 + SCAN_TILE - 1) / SCAN_TILE);
     if (tiles > 0) {
         async_wait<SCAN_STAGES - 2>();
@@ -440,7 +477,7 @@ __global__ void __launch_bounds__(32, NPT <= 4 ? 12 : 8) scan_walk_kernel(ScanAr
     }
     for (int tile = 0; tile < tiles; ++tile) {
         if (OUT) tile_outputs(tile + SCAN_STAGES - 1);  // of the tile before this one
-        tile_steps(tile + 1);
+        tile_steps(tile + 1);  // adds this tile's steps to the chunk's
         wide_rows(tile + 1);
         const float* Bs = (WIDE ? sh.B : reinterpret_cast<const float*>(sh.st[tile % SCAN_STAGES].B)) + L.n0;
         const float* Cs = (WIDE ? sh.C : reinterpret_cast<const float*>(sh.st[tile % SCAN_STAGES].C)) + L.n0;
@@ -492,6 +529,8 @@ __global__ void __launch_bounds__(32, NPT <= 4 ? 12 : 8) scan_walk_kernel(ScanAr
         }
         put_steps();
         put_rows();
+        if (!OUT && (tile + 1) * SCAN_TILE % a.chunk == 0)
+            emit(blockIdx.y * (a.run / a.chunk) + (tile + 1) * SCAN_TILE / a.chunk - 1);
         fetch(tile + SCAN_STAGES - 1);  // into the stage of the tile before this one
         async_wait<SCAN_STAGES - 3>();  // the tile after the next is there
         __syncwarp();
@@ -500,70 +539,62 @@ __global__ void __launch_bounds__(32, NPT <= 4 ? 12 : 8) scan_walk_kernel(ScanAr
         tile_outputs(tiles - 1);
         put_outputs(tiles - 1);
     }
+    if (!OUT) {  // the chunks that end behind the last whole one, the empty ones among them
+        const int first = blockIdx.y * (a.run / a.chunk) + tiles * SCAN_TILE / a.chunk;
+        const int last = min((int)(blockIdx.y + 1) * (a.run / a.chunk), a.nchunk);
+        for (int k = first; k < last; ++k) emit(k);
+    }
     if (OUT) {
         if (state && t1 == len) {
 #pragma unroll
             for (int i = 0; i < NP; ++i) unpack2(h[i], tmp[2 * i], tmp[2 * i + 1]);
             L.store(state, a.N, tmp);
         }
-    } else {
-#pragma unroll
-        for (int i = 0; i < NP; ++i) unpack2(h[i], tmp[2 * i], tmp[2 * i + 1]);
-        L.store(a.E + at * a.N, a.N, tmp);
-        if (REV) {
-#pragma unroll
-            for (int i = 0; i < NP; ++i) unpack2(r[i], tmp[2 * i], tmp[2 * i + 1]);
-            L.store(a.R + at * a.N, a.N, tmp);
-        }
-        float s0, s1;
-        unpack2(steps, s0, s1);
-#pragma unroll
-        for (int m = WCH / 2; m < 32; m <<= 1) {
-            s0 += __shfl_xor_sync(0xffffffffu, s0, m);
-            s1 += __shfl_xor_sync(0xffffffffu, s1, m);
-        }
-        if (lane < WCH / 2) {
-            float* S = a.S + ((long long)L.b * a.nchunk + blockIdx.y) * a.D + L.c0;
-            if (ic < L.cols) S[ic] = s0;
-            if (ic + 1 < L.cols) S[ic + 1] = s1;
-        }
     }
 }
 
-// Chains the chunks: E[k] becomes the state that chunk k starts from and, in the gradient, R[k]
-// the carry that reaches its last token.  One thread a state; the loads of SCAN_AHEAD chunks are
-// in flight together.
+// Chains the chunks: E[k] becomes the state that chunk k starts from and, in the gradient (the
+// grid's second row), R[k] the carry that reaches its last token.  One thread a state; the loads of
+// SCAN_AHEAD chunks are in flight together.  Bound by memory.
 constexpr int SCAN_AHEAD = 8;
 template <typename T>
-__global__ void __launch_bounds__(256) scan_carry_kernel(ScanArgs<T> a, int rev) {
+__global__ void __launch_bounds__(256) scan_carry_kernel(ScanArgs<T> a) {
+    const bool rev = blockIdx.y;
     const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
     const long long dn = (long long)a.D * a.N;
     if (i >= a.B * dn) return;
     const long long b = i / dn, cn = i % dn;
     const float A2 = a.A[cn] * kLog2e;
-    float* E = (rev ? a.R : a.E) + b * a.nchunk * dn + cn;
-    const float* S = a.S + b * a.nchunk * a.D + cn / a.N;
+    const long long last = a.nchunk - 1;
+    const long long step = rev ? -1 : 1;
+    float* E = (rev ? a.R : a.E) + (b * a.nchunk + (rev ? last : 0)) * dn + cn;
+    const float* S = a.S + (b * a.nchunk + (rev ? last : 0)) * a.D + cn / a.N;
     float h = 0.f;
     if (rev) {
         if (a.dstate_end) h = a.dstate_end[i];
     } else if (a.state && !a.fresh) {
         h = a.state[i];
     }
-    for (int k = 0; k < a.nchunk; k += SCAN_AHEAD) {
-        float e[SCAN_AHEAD], s[SCAN_AHEAD];
+    float e[SCAN_AHEAD], s[SCAN_AHEAD];
+    auto fetch = [&](long long k) {
 #pragma unroll
         for (int q = 0; q < SCAN_AHEAD; ++q)
-            if (k + q < a.nchunk - 1) {  // the last chunk's effect is not needed
-                const long long at = rev ? a.nchunk - 1 - (k + q) : k + q;
-                e[q] = E[at * dn];
-                s[q] = S[at * a.D];
+            if (k + q < last) {  // the last chunk's effect is not needed
+                e[q] = E[(k + q) * step * dn];
+                s[q] = S[(k + q) * step * a.D];
             }
+    };
+    fetch(0);
+    for (long long k = 0; k <= last; k += SCAN_AHEAD) {
+        float ce[SCAN_AHEAD], cs[SCAN_AHEAD];
+#pragma unroll
+        for (int q = 0; q < SCAN_AHEAD; ++q) ce[q] = e[q], cs[q] = s[q];
+        fetch(k + SCAN_AHEAD);
 #pragma unroll
         for (int q = 0; q < SCAN_AHEAD; ++q)
-            if (k + q < a.nchunk) {
-                const long long at = rev ? a.nchunk - 1 - (k + q) : k + q;
-                E[at * dn] = h;
-                if (k + q < a.nchunk - 1) h = fmaf(exp2_fast(s[q] * A2), h, e[q]);
+            if (k + q <= last) {
+                E[(k + q) * step * dn] = h;
+                if (k + q < last) h = fmaf(exp2_fast(cs[q] * A2), h, ce[q]);
             }
     }
 }

@@ -287,12 +287,12 @@ ScanArgs<T> scan_args(const sdm_scan_dims* d, const sdm_view* u, const sdm_view*
 }
 
 template <typename T, int NPT, int LN, int MODE>
-sdm_status launch_walk(const ScanArgs<T>& a, int chunks, cudaStream_t s) {
+sdm_status launch_walk(const ScanArgs<T>& a, int runs, cudaStream_t s) {
     constexpr int WCH = 32 / LN;
     constexpr size_t smem = sizeof(ScanShared<T, NPT * LN, WCH, MODE>);
     if (!allow_smem(scan_walk_kernel<T, NPT, LN, MODE>, smem)) return SDM_ERR_CUDA;
     const unsigned gx = (unsigned)(a.G * ceil_div(a.D / a.G, WCH));
-    scan_walk_kernel<T, NPT, LN, MODE><<<dim3(gx, chunks, a.B), 32, smem, s>>>(a);
+    scan_walk_kernel<T, NPT, LN, MODE><<<dim3(gx, runs, a.B), 32, smem, s>>>(a);
     return launched();
 }
 
@@ -303,7 +303,7 @@ sdm_status launch_scan_t(ScanArgs<T> a, const sdm_view* const (&v)[6], cudaStrea
         const sdm_status e = launch_walk<T, NPT, LN, SCAN_CHUNK>(a, a.nchunk - 1, s);
         if (e) return e;
         const long long n = (long long)a.B * a.D * a.N;
-        scan_carry_kernel<T><<<(unsigned)ceil_div(n, 256), 256, 0, s>>>(a, 0);
+        scan_carry_kernel<T><<<(unsigned)ceil_div(n, 256), 256, 0, s>>>(a);
     }
     return launch_walk<T, NPT, LN, SCAN_OUT>(a, a.nchunk, s);
 }
@@ -327,7 +327,7 @@ sdm_status run_scan(const sdm_scan_dims* d, ScanArgs<T> a, const sdm_view* const
         return launched();
     }
     const ScanPlan p = scan_plan(d);
-    a.chunk = p.chunk, a.nchunk = p.nchunk;
+    a.chunk = a.run = p.chunk, a.nchunk = p.nchunk;
     a.E = static_cast<float*>(ws);
     a.S = reinterpret_cast<float*>(static_cast<char*>(ws) + p.off_S);
     if (p.LN * 8 == p.NN) {
@@ -354,11 +354,13 @@ ScanBwdPlan scan_bwd_plan(const sdm_scan_dims* d) {
     ScanBwdPlan p{};
     p.NN = pad_states(d->N);
     p.nchunk = (int)std::max(1LL, ceil_div(d->T, BWD_CHUNK));
-    // a block's channels by turns of its warps: more turns, fewer shares of dB and dC to write and
-    // add; as many as leave six blocks an SM, two for each of the three that fit
+    // A block's channels go by turns of its warps: more turns, fewer shares of dB and dC to write and
+    // add; fewer turns, more blocks to even the SMs' work out.  Fourteen blocks an SM, of which
+    // three run at a time, did best (2 sequences of 2048 tokens, 2048 channels: 361 us in 2048
+    // blocks, 368 us in 896, 390 us in 384, 407 us in 8192).
     const int ch = BWD_WARPS * 32 / (p.NN / 4), all = (int)ceil_div(d->D / d->G, ch);
     const long long rest = (long long)d->B * p.nchunk * d->G;
-    const long long want = std::max(1LL, std::min<long long>(all, ceil_div(6 * kSms, rest)));
+    const long long want = std::max(1LL, std::min<long long>(all, 14 * kSms / rest));
     p.tiles = (int)ceil_div(all, want);
     p.blocks = (int)ceil_div(all, p.tiles);
     const size_t bk = (size_t)d->B * p.nchunk, states = bk * d->D * d->N * 4;
@@ -382,11 +384,15 @@ sdm_status launch_scan_bwd_t(const ScanBwdArgs<T>& A, const ScanBwdPlan& p,
     constexpr int NN = LN * BWD_NPT, CLN = NN / 8;
     if (p.nchunk > 1) {
         set_pieces(a, v, 32 / CLN, NN);
-        const sdm_status e = launch_walk<T, 8, CLN, SCAN_CHUNK_REV>(a, p.nchunk, s);
+        // a walk over several chunks keeps its tiles coming; runs for 16 warps an SM
+        const long long warps = (long long)a.B * a.G * ceil_div(a.D / a.G, 32 / CLN);
+        const long long runs = std::min<long long>(p.nchunk, ceil_div(16 * kSms, warps));
+        a.run = (int)ceil_div(p.nchunk, runs) * BWD_CHUNK;
+        const sdm_status e =
+            launch_walk<T, 8, CLN, SCAN_CHUNK_REV>(a, (int)ceil_div(p.nchunk, a.run / BWD_CHUNK), s);
         if (e) return e;
         const unsigned n = (unsigned)ceil_div((long long)a.B * a.D * a.N, 256);
-        scan_carry_kernel<T><<<n, 256, 0, s>>>(a, 0);
-        scan_carry_kernel<T><<<n, 256, 0, s>>>(a, 1);
+        scan_carry_kernel<T><<<dim3(n, 2), 256, 0, s>>>(a);
     }
     ScanBwdArgs<T> B = A;
     set_pieces(B.s, v, 32 / LN, NN);
