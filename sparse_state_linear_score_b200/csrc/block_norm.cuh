@@ -36,18 +36,20 @@ struct NormArgs {
     float eps;
 };
 
-// V values of a row as they are stored, in registers until they are used: a block's loads are all
-// in flight before the first is waited for.
-template <int V>
+constexpr int NORM_V = 4, NORM_P = 2;  // values of a piece, pieces of a thread
+
+// A piece of a row as it is stored, in registers until it is used: a block's loads are all in flight
+// before the first is waited for.  VEC: D is a multiple of four, so pieces are whole and aligned;
+// else they are loaded value by value, `cnt` of them.
+template <bool VEC>
 struct NormRaw {
-    static constexpr int N = (V + 1) / 2;
-    uint32_t x[V];
+    uint32_t x[4];
     SDM_DEV void clear() {
 #pragma unroll
-        for (int i = 0; i < V; ++i) x[i] = 0u;
+        for (int i = 0; i < 4; ++i) x[i] = 0u;
     }
-    SDM_DEV void load(const void* p, bool is_bf16, long long at) {
-        if constexpr (V == 4) {
+    SDM_DEV void load(const void* p, bool is_bf16, long long at, int cnt) {
+        if (VEC) {
             if (is_bf16) {
                 const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const bf16*>(p) + at);
                 x[0] = v.x, x[1] = v.y;
@@ -56,41 +58,54 @@ struct NormRaw {
                 x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
             }
         } else {
-            x[0] = is_bf16 ? static_cast<const uint16_t*>(p)[at] : static_cast<const uint32_t*>(p)[at];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i < cnt)
+                    x[i] = is_bf16 ? static_cast<const uint16_t*>(p)[at + i]
+                                   : static_cast<const uint32_t*>(p)[at + i];
         }
     }
-    SDM_DEV void get(bool is_bf16, f32x2 (&v)[N]) const {
-        if constexpr (V == 4) {
-            v[0] = is_bf16 ? pack2(bf16_lo(x[0]), bf16_hi(x[0]))
-                           : pack2(__uint_as_float(x[0]), __uint_as_float(x[1]));
-            v[1] = is_bf16 ? pack2(bf16_lo(x[1]), bf16_hi(x[1]))
-                           : pack2(__uint_as_float(x[2]), __uint_as_float(x[3]));
+    SDM_DEV void get(bool is_bf16, f32x2 (&v)[2]) const {
+        if (!is_bf16) {
+            v[0] = pack2(__uint_as_float(x[0]), __uint_as_float(x[1]));
+            v[1] = pack2(__uint_as_float(x[2]), __uint_as_float(x[3]));
+        } else if (VEC) {
+            v[0] = pack2(bf16_lo(x[0]), bf16_hi(x[0]));
+            v[1] = pack2(bf16_lo(x[1]), bf16_hi(x[1]));
         } else {
-            v[0] = pack2(is_bf16 ? bf16_lo(x[0]) : __uint_as_float(x[0]), 0.f);
+            v[0] = pack2(bf16_lo(x[0]), bf16_lo(x[1]));
+            v[1] = pack2(bf16_lo(x[2]), bf16_lo(x[3]));
         }
     }
 };
-template <int V>
-SDM_DEV void norm_store(void* p, bool is_bf16, long long at, const f32x2 (&v)[(V + 1) / 2]) {
-    float x[(V + 1) / 2 * 2], y[V];
+template <bool VEC>
+SDM_DEV void norm_store(void* p, bool is_bf16, long long at, int cnt, const f32x2 (&v)[2]) {
+    float x[4];
+    unpack2(v[0], x[0], x[1]);
+    unpack2(v[1], x[2], x[3]);
+    if (VEC) {
+        if (is_bf16) Vec<4>::store(static_cast<bf16*>(p) + at, x);
+        else Vec<4>::store(static_cast<float*>(p) + at, x);
+    } else {
 #pragma unroll
-    for (int i = 0; i < (V + 1) / 2; ++i) unpack2(v[i], x[2 * i], x[2 * i + 1]);
-#pragma unroll
-    for (int i = 0; i < V; ++i) y[i] = x[i];
-    if (is_bf16) Vec<V>::store(static_cast<bf16*>(p) + at, y);
-    else Vec<V>::store(static_cast<float*>(p) + at, y);
+        for (int i = 0; i < 4; ++i)
+            if (i < cnt) {
+                if (is_bf16) st(static_cast<bf16*>(p) + at + i, x[i]);
+                else st(static_cast<float*>(p) + at + i, x[i]);
+            }
+    }
 }
-// V entries of a weight vector (1 where there is none).
-template <int V>
-SDM_DEV void norm_weight(const float* w, int c, f32x2 (&v)[(V + 1) / 2]) {
-#pragma unroll
-    for (int i = 0; i < (V + 1) / 2; ++i) v[i] = dup2(1.f);
+// A piece of a weight vector (1 where there is none).
+template <bool VEC>
+SDM_DEV void norm_weight(const float* w, int c, int cnt, f32x2 (&v)[2]) {
+    v[0] = v[1] = dup2(1.f);
     if (!w) return;
-    if constexpr (V == 4) {
+    if (VEC || cnt == 4) {  // c is a multiple of four
         const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(w + c);
         v[0] = x.x, v[1] = x.y;
     } else {
-        v[0] = pack2(w[c], 0.f);
+        v[0] = pack2(w[c], cnt > 1 ? w[c + 1] : 1.f);
+        v[1] = pack2(cnt > 2 ? w[c + 2] : 1.f, 1.f);
     }
 }
 SDM_DEV float sum2(f32x2 v) {
@@ -189,11 +204,11 @@ struct NormPlace {
     }
 };
 
-// Piece i of thread t is column col0 + (i*blockDim + t)*V.  DT: which of r, f, x are bf16 (bits 0,
+// Piece i of thread t starts at column col0 + (i*blockDim + t)*4.  DT: which of r, f, x are bf16 (bits 0,
 // 1, 2), or -1: as the arguments say.
-template <int V, int P, bool CL, int DT>
+template <bool VEC, bool CL, int DT>
 __global__ void __launch_bounds__(NORM_THREADS, 2) block_norm_kernel(NormArgs a) {
-    constexpr int N = (V + 1) / 2;
+    constexpr int P = NORM_P, N = 2;
     __shared__ __align__(16) NormSums s_sum;
     const bool rb = DT < 0 ? a.rb : DT & 1, fb = DT < 0 ? a.fb : DT & 2, xb = DT < 0 ? a.xb : DT & 4;
     const NormPlace<CL> at;
@@ -203,17 +218,17 @@ __global__ void __launch_bounds__(NORM_THREADS, 2) block_norm_kernel(NormArgs a)
     const float inv_d = 1.f / (float)a.D;
     for (long long row = at.first; row < a.rows; row += at.step) {
         const long long base = row * a.D;
-        NormRaw<V> rf[P], rr[P], rg[P];
+        NormRaw<VEC> rf[P], rr[P], rg[P];
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-            const int c = at.col0 + (i * blockDim.x + threadIdx.x) * V;
+            const int c = at.col0 + (i * blockDim.x + threadIdx.x) * NORM_V, cnt = min(NORM_V, a.D - c);
             rf[i].clear();
             rr[i].clear();
             rg[i].clear();
             if (c < a.D) {
-                rf[i].load(a.f, fb, base + c);
-                rr[i].load(a.r, rb, base + c);
-                if (a.gate) rg[i].load(a.gate, xb, base + c);
+                rf[i].load(a.f, fb, base + c, cnt);
+                rr[i].load(a.r, rb, base + c, cnt);
+                if (a.gate) rg[i].load(a.gate, xb, base + c, cnt);
             }
         }
         f32x2 f[P][N], o[P][N], s2 = dup2(0.f);
@@ -233,11 +248,11 @@ __global__ void __launch_bounds__(NORM_THREADS, 2) block_norm_kernel(NormArgs a)
         s2 = dup2(0.f);
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-            const int c = at.col0 + (i * blockDim.x + threadIdx.x) * V;
+            const int c = at.col0 + (i * blockDim.x + threadIdx.x) * NORM_V, cnt = min(NORM_V, a.D - c);
             if (c < a.D) {
                 f32x2 wp[N], sc[N], g[N];
-                norm_weight<V>(a.w_post, c, wp);
-                norm_weight<V>(a.scale, c, sc);
+                norm_weight<VEC>(a.w_post, c, cnt, wp);
+                norm_weight<VEC>(a.scale, c, cnt, sc);
                 rg[i].get(xb, g);
                 rr[i].get(rb, o[i]);
 #pragma unroll
@@ -247,7 +262,7 @@ __global__ void __launch_bounds__(NORM_THREADS, 2) block_norm_kernel(NormArgs a)
                     o[i][v] = fma2(m, f[i][v], o[i][v]);
                     s2 = fma2(o[i][v], o[i][v], s2);
                 }
-                if (a.r_out) norm_store<V>(a.r_out, rb, base + c, o[i]);
+                if (a.r_out) norm_store<VEC>(a.r_out, rb, base + c, cnt, o[i]);
             }
         }
         if (!a.n) continue;
@@ -256,22 +271,22 @@ __global__ void __launch_bounds__(NORM_THREADS, 2) block_norm_kernel(NormArgs a)
         k = dup2(rsqrtf(ss[0] * inv_d + a.eps));
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-            const int c = at.col0 + (i * blockDim.x + threadIdx.x) * V;
+            const int c = at.col0 + (i * blockDim.x + threadIdx.x) * NORM_V, cnt = min(NORM_V, a.D - c);
             if (c < a.D) {
                 f32x2 wq[N];
-                norm_weight<V>(a.w_pre, c, wq);
+                norm_weight<VEC>(a.w_pre, c, cnt, wq);
 #pragma unroll
                 for (int v = 0; v < N; ++v) o[i][v] = mul2(o[i][v], mul2(k, wq[v]));
-                norm_store<V>(a.n, xb, base + c, o[i]);
+                norm_store<VEC>(a.n, xb, base + c, cnt, o[i]);
             }
         }
     }
     if (CL) cooperative_groups::this_cluster().sync();  // no block ends while others write to it
 }
 
-template <int V, int P, bool CL, int DT>
+template <bool VEC, bool CL, int DT>
 __global__ void __launch_bounds__(NORM_THREADS, 1) block_norm_bwd_kernel(NormArgs a) {
-    constexpr int N = (V + 1) / 2;
+    constexpr int P = NORM_P, N = 2;
     __shared__ __align__(16) NormSums s_sum;
     const bool rb = DT < 0 ? a.rb : DT & 1, fb = DT < 0 ? a.fb : DT & 2, xb = DT < 0 ? a.xb : DT & 4;
     const NormPlace<CL> at;
@@ -285,23 +300,23 @@ __global__ void __launch_bounds__(NORM_THREADS, 1) block_norm_bwd_kernel(NormArg
 #pragma unroll
         for (int v = 0; v < N; ++v) aw[i][v] = as[i][v] = aq[i][v] = zero;
     const float inv_d = 1.f / (float)a.D;
-    NormRaw<V> rf[P], rr[P], rg[P], rn[P], rd[P];
+    NormRaw<VEC> rf[P], rr[P], rg[P], rn[P], rd[P];
     auto fetch = [&](long long row) {
         const long long base = row * a.D;
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-            const int c = at.col0 + (i * blockDim.x + threadIdx.x) * V;
+            const int c = at.col0 + (i * blockDim.x + threadIdx.x) * NORM_V, cnt = min(NORM_V, a.D - c);
             rf[i].clear();
             rr[i].clear();
             rg[i].clear();
             rn[i].clear();
             rd[i].clear();
             if (c < a.D && row < a.rows) {
-                rf[i].load(a.f, fb, base + c);
-                rr[i].load(a.r, rb, base + c);
-                if (a.gate) rg[i].load(a.gate, xb, base + c);
-                if (a.dn) rn[i].load(a.dn, xb, base + c);
-                if (a.dr_out) rd[i].load(a.dr_out, rb, base + c);
+                rf[i].load(a.f, fb, base + c, cnt);
+                rr[i].load(a.r, rb, base + c, cnt);
+                if (a.gate) rg[i].load(a.gate, xb, base + c, cnt);
+                if (a.dn) rn[i].load(a.dn, xb, base + c, cnt);
+                if (a.dr_out) rd[i].load(a.dr_out, rb, base + c, cnt);
             }
         }
     };
@@ -339,12 +354,12 @@ __global__ void __launch_bounds__(NORM_THREADS, 1) block_norm_bwd_kernel(NormArg
         // f becomes f^ (f itself without the norm), g the gate's sigmoid
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-            const int c = at.col0 + (i * blockDim.x + threadIdx.x) * V;
+            const int c = at.col0 + (i * blockDim.x + threadIdx.x) * NORM_V, cnt = min(NORM_V, a.D - c);
             if (c >= a.D) continue;
             f32x2 wp[N], sc[N], wq[N];
-            norm_weight<V>(a.w_post, c, wp);
-            norm_weight<V>(a.scale, c, sc);
-            norm_weight<V>(a.w_pre, c, wq);
+            norm_weight<VEC>(a.w_post, c, cnt, wp);
+            norm_weight<VEC>(a.scale, c, cnt, sc);
+            norm_weight<VEC>(a.w_pre, c, cnt, wq);
 #pragma unroll
             for (int v = 0; v < N; ++v) {
                 f[i][v] = mul2(f[i][v], rf1);
@@ -374,12 +389,12 @@ __global__ void __launch_bounds__(NORM_THREADS, 1) block_norm_bwd_kernel(NormArg
         }
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-            const int c = at.col0 + (i * blockDim.x + threadIdx.x) * V;
+            const int c = at.col0 + (i * blockDim.x + threadIdx.x) * NORM_V, cnt = min(NORM_V, a.D - c);
             if (c >= a.D) continue;
             f32x2 wp[N], sc[N], wq[N], dg[N];
-            norm_weight<V>(a.w_post, c, wp);
-            norm_weight<V>(a.scale, c, sc);
-            norm_weight<V>(a.w_pre, c, wq);
+            norm_weight<VEC>(a.w_post, c, cnt, wp);
+            norm_weight<VEC>(a.scale, c, cnt, sc);
+            norm_weight<VEC>(a.w_pre, c, cnt, wq);
 #pragma unroll
             for (int v = 0; v < N; ++v) {
                 const f32x2 oh = mul2(o[i][v], ro);
@@ -394,19 +409,19 @@ __global__ void __launch_bounds__(NORM_THREADS, 1) block_norm_bwd_kernel(NormArg
                 aw[i][v] = fma2(dp, f[i][v], aw[i][v]);
                 o[i][v] = mul2(rf1, fma2(f[i][v], mf, mul2(dp, wp[v])));
             }
-            if (a.dr) norm_store<V>(a.dr, rb, base + c, dr[i]);
-            if (a.dgate) norm_store<V>(a.dgate, xb, base + c, dg);
-            if (a.df) norm_store<V>(a.df, fb, base + c, o[i]);
+            if (a.dr) norm_store<VEC>(a.dr, rb, base + c, cnt, dr[i]);
+            if (a.dgate) norm_store<VEC>(a.dgate, xb, base + c, cnt, dg);
+            if (a.df) norm_store<VEC>(a.df, fb, base + c, cnt, o[i]);
         }
     }
     float* part = a.part + at.first * 3 * a.D;
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-        const int c = at.col0 + (i * blockDim.x + threadIdx.x) * V;
-        if (c < a.D) {  // V = 4: D is a multiple of 4
-            norm_store<V>(part, false, c, as[i]);
-            norm_store<V>(part, false, (long long)a.D + c, aw[i]);
-            norm_store<V>(part, false, 2LL * a.D + c, aq[i]);
+        const int c = at.col0 + (i * blockDim.x + threadIdx.x) * NORM_V, cnt = min(NORM_V, a.D - c);
+        if (c < a.D) {
+            norm_store<VEC>(part, false, c, cnt, as[i]);
+            norm_store<VEC>(part, false, (long long)a.D + c, cnt, aw[i]);
+            norm_store<VEC>(part, false, 2LL * a.D + c, cnt, aq[i]);
         }
     }
     if (CL) cooperative_groups::this_cluster().sync();

@@ -494,9 +494,8 @@ NormPlan norm_plan(const sdm_norm_dims* d, bool bwd) {
     return p;
 }
 
-template <int V, bool CL, int DT>
+template <bool VEC, bool CL, int DT>
 sdm_status launch_norm(const NormArgs& a, bool bwd, const NormPlan& p, cudaStream_t s) {
-    constexpr int P = 8 / V;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
     attr.val.clusterDim.x = p.blocks, attr.val.clusterDim.y = 1, attr.val.clusterDim.z = 1;
@@ -506,26 +505,26 @@ sdm_status launch_norm(const NormArgs& a, bool bwd, const NormPlan& p, cudaStrea
     cfg.stream = s;
     cfg.attrs = &attr;
     cfg.numAttrs = CL ? 1 : 0;
-    const cudaError_t e = bwd ? cudaLaunchKernelEx(&cfg, block_norm_bwd_kernel<V, P, CL, DT>, a)
-                              : cudaLaunchKernelEx(&cfg, block_norm_kernel<V, P, CL, DT>, a);
+    const cudaError_t e = bwd ? cudaLaunchKernelEx(&cfg, block_norm_bwd_kernel<VEC, CL, DT>, a)
+                              : cudaLaunchKernelEx(&cfg, block_norm_kernel<VEC, CL, DT>, a);
     (void)cudaGetLastError();
     return e == cudaSuccess ? SDM_OK : SDM_ERR_CUDA;
 }
 
 sdm_status launch_norm_any(const NormArgs& a, bool bwd, const NormPlan& p, cudaStream_t s) {
     if (a.D % 4 != 0)
-        return p.blocks > 1 ? launch_norm<1, true, -1>(a, bwd, p, s)
-                            : launch_norm<1, false, -1>(a, bwd, p, s);
-    if (p.blocks > 1) return launch_norm<4, true, -1>(a, bwd, p, s);
+        return p.blocks > 1 ? launch_norm<false, true, -1>(a, bwd, p, s)
+                            : launch_norm<false, false, -1>(a, bwd, p, s);
+    if (p.blocks > 1) return launch_norm<true, true, -1>(a, bwd, p, s);
     switch (a.rb | a.fb << 1 | a.xb << 2) {
-        case 0: return launch_norm<4, false, 0>(a, bwd, p, s);
-        case 1: return launch_norm<4, false, 1>(a, bwd, p, s);
-        case 2: return launch_norm<4, false, 2>(a, bwd, p, s);
-        case 3: return launch_norm<4, false, 3>(a, bwd, p, s);
-        case 4: return launch_norm<4, false, 4>(a, bwd, p, s);
-        case 5: return launch_norm<4, false, 5>(a, bwd, p, s);
-        case 6: return launch_norm<4, false, 6>(a, bwd, p, s);
-        default: return launch_norm<4, false, 7>(a, bwd, p, s);
+        case 0: return launch_norm<true, false, 0>(a, bwd, p, s);
+        case 1: return launch_norm<true, false, 1>(a, bwd, p, s);
+        case 2: return launch_norm<true, false, 2>(a, bwd, p, s);
+        case 3: return launch_norm<true, false, 3>(a, bwd, p, s);
+        case 4: return launch_norm<true, false, 4>(a, bwd, p, s);
+        case 5: return launch_norm<true, false, 5>(a, bwd, p, s);
+        case 6: return launch_norm<true, false, 6>(a, bwd, p, s);
+        default: return launch_norm<true, false, 7>(a, bwd, p, s);
     }
 }
 
