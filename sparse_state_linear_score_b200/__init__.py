@@ -671,13 +671,12 @@ def _new_rows(like, lens):
 
 
 def _new_like(t):
-    return torch.empty_like(t) if t.is_contiguous() else \
-        torch.empty(t.shape, dtype=t.dtype, device=t.device)
+    return torch.empty_like(t) if t.is_contiguous() else t.new_empty(t.shape)
 
 
 def _scratch(ws, nbytes, like):
     if ws is None:
-        ws = torch.empty(max(16, nbytes), dtype=torch.uint8, device=like.device)
+        ws = like.new_empty(max(16, nbytes), dtype=torch.uint8)
     elif ws.get_device() != like.get_device():
         raise ValueError(f"ws is on {ws.device}, the inputs on {like.device}")
     return ws, _ptr(ws, "ws"), ws.numel() * ws.element_size()
@@ -738,13 +737,11 @@ def short_conv_backward(x, w, dy, bias=None, act="silu", state=None, lens=None, 
     dev, shape, dt = x.get_device(), x.shape, x.dtype
     B, H, T, d = shape
     st = (B, H, K - 1, d)
-    f = dict(dtype=torch.float32, device=x.device)
-    g = {"dx": _new_like(x) if dx is None else dx,
-         "dw": torch.empty((H, d, K), **f)}
+    g = {"dx": _new_like(x) if dx is None else dx, "dw": x.new_empty((H, d, K), dtype=torch.float32)}
     if bias is not None:
-        g["dbias"] = torch.empty((H, d), **f)
+        g["dbias"] = x.new_empty((H, d), dtype=torch.float32)
     if state is not None:
-        g["dstate"] = torch.empty(st, **f)
+        g["dstate"] = x.new_empty(st, dtype=torch.float32)
     ws, wp, wn = _scratch(ws, need, x)
     _ok(_lib.sdm_short_conv_backward(
         c, _heads(x, "x", shape, dt, dev), _arg(w, "w", (H, d, K), torch.float32, dev),
@@ -821,19 +818,16 @@ def selective_scan_backward(u, delta, A, B, C, dy, D=None, z=None, dt_bias=None,
     inputs = _scan_inputs(c, u, delta, A, B, C, D, z, dt_bias, state, lens)
     dev, dt, rows, f32 = u.get_device(), u.dtype, u.shape, torch.float32
     gn, st = (c.B, c.T, c.G, c.N), (c.B, c.D, c.N)
-
-    def new(shape, dtype):
-        return torch.empty(shape, dtype=dtype, device=u.device)
-    g = {"du": new(rows, dt), "ddelta": new(rows, dt), "dA": new((c.D, c.N), f32),
-         "dB": new(gn, dt), "dC": new(gn, dt)}
+    g = {"du": u.new_empty(rows), "ddelta": u.new_empty(rows), "dA": torch.empty_like(A),
+         "dB": u.new_empty(gn), "dC": u.new_empty(gn)}
     if D is not None:
-        g["dD"] = new((c.D,), f32)
+        g["dD"] = torch.empty_like(D)
     if z is not None:
-        g["dz"] = new(rows, dt)
+        g["dz"] = u.new_empty(rows)
     if dt_bias is not None:
-        g["ddt_bias"] = new((c.D,), f32)
+        g["ddt_bias"] = torch.empty_like(dt_bias)
     if state is not None:
-        g["dstate"] = new(st, f32)
+        g["dstate"] = torch.empty_like(state)
     ws, wp, wn = _scratch(ws, need, u)
 
     def p(name):
@@ -908,7 +902,7 @@ def block_norm_backward(r, f, dr_out, dn, w_post=None, gate=None, scale=None, w_
         g["dgate"] = _new_like(gate)
     for name, w in (("dscale", scale), ("dw_post", w_post), ("dw_pre", w_pre)):
         if w is not None:
-            g[name] = torch.empty(col, dtype=f32, device=r.device)
+            g[name] = torch.empty_like(w)
 
     def p(name):
         return g[name].data_ptr() if name in g else None
