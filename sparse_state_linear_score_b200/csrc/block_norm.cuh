@@ -97,9 +97,9 @@ SDM_DEV void norm_store(void* p, bool is_bf16, long long at, int cnt, const f32x
 }
 // A piece of a weight vector (1 where there is none).
 template <bool VEC>
-SDM_DEV void norm_weight(const float* w, int c, int cnt, f32x2 (&v)[2]) {
+SDM_DEV void norm_weight(bool has, const float* w, int c, int cnt, f32x2 (&v)[2]) {
     v[0] = v[1] = dup2(1.f);
-    if (!w) return;
+    if (!has) return;
     if (VEC || cnt == 4) {  // c is a multiple of four
         const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(w + c);
         v[0] = x.x, v[1] = x.y;
@@ -205,12 +205,14 @@ struct NormPlace {
 };
 
 // Piece i of thread t starts at column col0 + (i*blockDim + t)*4.  DT: which of r, f, x are bf16 (bits 0,
-// 1, 2), or -1: as the arguments say.
-template <bool VEC, bool CL, int DT>
+// 1, 2), or -1: as the arguments say.  ALL: no argument is missing.
+template <bool VEC, bool CL, int DT, bool ALL>
 __global__ void __launch_bounds__(NORM_THREADS, 2) block_norm_kernel(NormArgs a) {
     constexpr int P = NORM_P, N = 2;
     __shared__ __align__(16) NormSums s_sum;
     const bool rb = DT < 0 ? a.rb : DT & 1, fb = DT < 0 ? a.fb : DT & 2, xb = DT < 0 ? a.xb : DT & 4;
+    const bool has_gate = ALL || a.gate, has_post = ALL || a.w_post, has_scale = ALL || a.scale,
+               has_pre = ALL || a.w_pre, out_r = ALL || a.r_out, out_n = ALL || a.n;
     const NormPlace<CL> at;
     RowSum<CL> red{s_sum, 0, at.rank, at.ranks};
     s_sum.clear();
@@ -228,7 +230,7 @@ __global__ void __launch_bounds__(NORM_THREADS, 2) block_norm_kernel(NormArgs a)
             if (c < a.D) {
                 rf[i].load(a.f, fb, base + c, cnt);
                 rr[i].load(a.r, rb, base + c, cnt);
-                if (a.gate) rg[i].load(a.gate, xb, base + c, cnt);
+                if (has_gate) rg[i].load(a.gate, xb, base + c, cnt);
             }
         }
         f32x2 f[P][N], o[P][N], s2 = dup2(0.f);
@@ -240,7 +242,7 @@ __global__ void __launch_bounds__(NORM_THREADS, 2) block_norm_kernel(NormArgs a)
             for (int v = 0; v < N; ++v) s2 = fma2(f[i][v], f[i][v], s2);
         }
         f32x2 k = dup2(1.f);
-        if (a.w_post) {
+        if (has_post) {
             ss[0] = sum2(s2);
             red.sum(ss);
             k = dup2(rsqrtf(ss[0] * inv_d + a.eps));
@@ -251,21 +253,21 @@ __global__ void __launch_bounds__(NORM_THREADS, 2) block_norm_kernel(NormArgs a)
             const int c = at.col0 + (i * blockDim.x + threadIdx.x) * NORM_V, cnt = min(NORM_V, a.D - c);
             if (c < a.D) {
                 f32x2 wp[N], sc[N], g[N];
-                norm_weight<VEC>(a.w_post, c, cnt, wp);
-                norm_weight<VEC>(a.scale, c, cnt, sc);
+                norm_weight<VEC>(has_post, a.w_post, c, cnt, wp);
+                norm_weight<VEC>(has_scale, a.scale, c, cnt, sc);
                 rg[i].get(xb, g);
                 rr[i].get(rb, o[i]);
 #pragma unroll
                 for (int v = 0; v < N; ++v) {
                     f32x2 m = mul2(mul2(sc[v], wp[v]), k);
-                    if (a.gate) m = mul2(m, sigmoid2(g[v]));
+                    if (has_gate) m = mul2(m, sigmoid2(g[v]));
                     o[i][v] = fma2(m, f[i][v], o[i][v]);
                     s2 = fma2(o[i][v], o[i][v], s2);
                 }
-                if (a.r_out) norm_store<VEC>(a.r_out, rb, base + c, cnt, o[i]);
+                if (out_r) norm_store<VEC>(a.r_out, rb, base + c, cnt, o[i]);
             }
         }
-        if (!a.n) continue;
+        if (!out_n) continue;
         ss[0] = sum2(s2);
         red.sum(ss);
         k = dup2(rsqrtf(ss[0] * inv_d + a.eps));
@@ -274,7 +276,7 @@ __global__ void __launch_bounds__(NORM_THREADS, 2) block_norm_kernel(NormArgs a)
             const int c = at.col0 + (i * blockDim.x + threadIdx.x) * NORM_V, cnt = min(NORM_V, a.D - c);
             if (c < a.D) {
                 f32x2 wq[N];
-                norm_weight<VEC>(a.w_pre, c, cnt, wq);
+                norm_weight<VEC>(has_pre, a.w_pre, c, cnt, wq);
 #pragma unroll
                 for (int v = 0; v < N; ++v) o[i][v] = mul2(o[i][v], mul2(k, wq[v]));
                 norm_store<VEC>(a.n, xb, base + c, cnt, o[i]);
@@ -284,11 +286,14 @@ __global__ void __launch_bounds__(NORM_THREADS, 2) block_norm_kernel(NormArgs a)
     if (CL) cooperative_groups::this_cluster().sync();  // no block ends while others write to it
 }
 
-template <bool VEC, bool CL, int DT>
+template <bool VEC, bool CL, int DT, bool ALL>
 __global__ void __launch_bounds__(NORM_THREADS, 1) block_norm_bwd_kernel(NormArgs a) {
     constexpr int P = NORM_P, N = 2;
     __shared__ __align__(16) NormSums s_sum;
     const bool rb = DT < 0 ? a.rb : DT & 1, fb = DT < 0 ? a.fb : DT & 2, xb = DT < 0 ? a.xb : DT & 4;
+    const bool has_gate = ALL || a.gate, has_post = ALL || a.w_post, has_scale = ALL || a.scale,
+               has_pre = ALL || a.w_pre, has_dn = ALL || a.dn, has_dr = ALL || a.dr_out,
+               out_dr = ALL || a.dr, out_df = ALL || a.df, out_dg = ALL || a.dgate;
     const NormPlace<CL> at;
     RowSum<CL> red{s_sum, 0, at.rank, at.ranks};
     s_sum.clear();
@@ -314,9 +319,9 @@ __global__ void __launch_bounds__(NORM_THREADS, 1) block_norm_bwd_kernel(NormArg
             if (c < a.D && row < a.rows) {
                 rf[i].load(a.f, fb, base + c, cnt);
                 rr[i].load(a.r, rb, base + c, cnt);
-                if (a.gate) rg[i].load(a.gate, xb, base + c, cnt);
-                if (a.dn) rn[i].load(a.dn, xb, base + c, cnt);
-                if (a.dr_out) rd[i].load(a.dr_out, rb, base + c, cnt);
+                if (has_gate) rg[i].load(a.gate, xb, base + c, cnt);
+                if (has_dn) rn[i].load(a.dn, xb, base + c, cnt);
+                if (has_dr) rd[i].load(a.dr_out, rb, base + c, cnt);
             }
         }
     };
@@ -335,11 +340,11 @@ __global__ void __launch_bounds__(NORM_THREADS, 1) block_norm_bwd_kernel(NormArg
         }
         return sum2(s2);
     };
-    float next[1] = {a.w_post ? square() : 0.f};
-    if (a.w_post) red.sum(next);
+    float next[1] = {has_post ? square() : 0.f};
+    if (has_post) red.sum(next);
     for (long long row = at.first; row < a.rows; row += at.step) {
         const long long base = row * a.D;
-        const f32x2 rf1 = a.w_post ? dup2(rsqrtf(next[0] * inv_d + a.eps)) : one;
+        const f32x2 rf1 = has_post ? dup2(rsqrtf(next[0] * inv_d + a.eps)) : one;
         f32x2 f[P][N], o[P][N], g[P][N], dn[P][N], dr[P][N];
         f32x2 so = zero, sm = zero, sma = zero, soa = zero, sda = zero;
 #pragma unroll
@@ -357,13 +362,13 @@ __global__ void __launch_bounds__(NORM_THREADS, 1) block_norm_bwd_kernel(NormArg
             const int c = at.col0 + (i * blockDim.x + threadIdx.x) * NORM_V, cnt = min(NORM_V, a.D - c);
             if (c >= a.D) continue;
             f32x2 wp[N], sc[N], wq[N];
-            norm_weight<VEC>(a.w_post, c, cnt, wp);
-            norm_weight<VEC>(a.scale, c, cnt, sc);
-            norm_weight<VEC>(a.w_pre, c, cnt, wq);
+            norm_weight<VEC>(has_post, a.w_post, c, cnt, wp);
+            norm_weight<VEC>(has_scale, a.scale, c, cnt, sc);
+            norm_weight<VEC>(has_pre, a.w_pre, c, cnt, wq);
 #pragma unroll
             for (int v = 0; v < N; ++v) {
                 f[i][v] = mul2(f[i][v], rf1);
-                g[i][v] = a.gate ? sigmoid2(g[i][v]) : one;
+                g[i][v] = has_gate ? sigmoid2(g[i][v]) : one;
                 const f32x2 k = mul2(mul2(sc[v], g[i][v]), mul2(f[i][v], wp[v])), m = mul2(dn[i][v], wq[v]);
                 o[i][v] = add2(k, o[i][v]);
                 so = fma2(o[i][v], o[i][v], so);
@@ -374,27 +379,27 @@ __global__ void __launch_bounds__(NORM_THREADS, 1) block_norm_bwd_kernel(NormArg
             }
         }
         f32x2 ro = zero, mo = zero, mf = zero;
-        if (a.dn || a.w_post) {
-            float st[6] = {sum2(so), sum2(sm), sum2(sma), sum2(soa), sum2(sda), a.w_post ? square() : 0.f};
+        if (has_dn || has_post) {
+            float st[6] = {sum2(so), sum2(sm), sum2(sma), sum2(soa), sum2(sda), has_post ? square() : 0.f};
             red.sum(st);
             next[0] = st[5];
             float q = 0.f, mean = 0.f;
-            if (a.dn) {
+            if (has_dn) {
                 q = rsqrtf(st[0] * inv_d + a.eps);
                 mean = st[1] * q * inv_d;  // mean(m o^)
             }
             ro = dup2(q);
             mo = dup2(-mean);
-            if (a.w_post) mf = dup2(-(st[4] + q * (st[2] - q * mean * st[3])) * inv_d);
+            if (has_post) mf = dup2(-(st[4] + q * (st[2] - q * mean * st[3])) * inv_d);
         }
 #pragma unroll
         for (int i = 0; i < P; ++i) {
             const int c = at.col0 + (i * blockDim.x + threadIdx.x) * NORM_V, cnt = min(NORM_V, a.D - c);
             if (c >= a.D) continue;
             f32x2 wp[N], sc[N], wq[N], dg[N];
-            norm_weight<VEC>(a.w_post, c, cnt, wp);
-            norm_weight<VEC>(a.scale, c, cnt, sc);
-            norm_weight<VEC>(a.w_pre, c, cnt, wq);
+            norm_weight<VEC>(has_post, a.w_post, c, cnt, wp);
+            norm_weight<VEC>(has_scale, a.scale, c, cnt, sc);
+            norm_weight<VEC>(has_pre, a.w_pre, c, cnt, wq);
 #pragma unroll
             for (int v = 0; v < N; ++v) {
                 const f32x2 oh = mul2(o[i][v], ro);
@@ -409,9 +414,9 @@ __global__ void __launch_bounds__(NORM_THREADS, 1) block_norm_bwd_kernel(NormArg
                 aw[i][v] = fma2(dp, f[i][v], aw[i][v]);
                 o[i][v] = mul2(rf1, fma2(f[i][v], mf, mul2(dp, wp[v])));
             }
-            if (a.dr) norm_store<VEC>(a.dr, rb, base + c, cnt, dr[i]);
-            if (a.dgate) norm_store<VEC>(a.dgate, xb, base + c, cnt, dg);
-            if (a.df) norm_store<VEC>(a.df, fb, base + c, cnt, o[i]);
+            if (out_dr) norm_store<VEC>(a.dr, rb, base + c, cnt, dr[i]);
+            if (out_dg) norm_store<VEC>(a.dgate, xb, base + c, cnt, dg);
+            if (out_df) norm_store<VEC>(a.df, fb, base + c, cnt, o[i]);
         }
     }
     float* part = a.part + at.first * 3 * a.D;

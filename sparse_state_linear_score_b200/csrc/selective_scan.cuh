@@ -75,9 +75,14 @@ SDM_DEV void spread_sum(float (&v)[SCAN_GRP], int nl) {
 // Copies W elements of each of TILE rows of a view (tokens t.., zero from t1 on and behind
 // `cols`) to shared memory, by the warp, tile after tile.  Where the rows allow whole pieces of
 // PIECE bytes a lane copies the same pieces of every tile and keeps their address, so that a piece
-// costs a comparison, an addition and the copy.
-template <typename T, int W, int TILE>
+// costs a comparison, an addition and the copy.  Rows of bf16 at odd addresses (an odd width or
+// stride) cannot go asynchronously: with HOLD a lane loads its elements of a tile to registers and
+// stores them when the next tile is fetched, so that it does not wait for them either.
+template <typename T, int W, int TILE, bool HOLD = false>
 struct RowCopy {
+    static constexpr int HELD = HOLD ? (TILE * W + 31) / 32 : 1;
+    T held[HELD];
+    T* held_for;
     static constexpr int ROW = W * (int)sizeof(T), PIECE = ROW < 16 ? ROW : 16, PER = ROW / PIECE;
     static constexpr int ITER = (TILE * PER + 31) / 32, RSTEP = 32 / PER;  // rows between a lane's pieces
     static_assert(PER <= 32 && (PER & (PER - 1)) == 0, "pieces of a row");
@@ -91,6 +96,7 @@ struct RowCopy {
         p = r.v.p + at + t0 * stride;
         piece = r.piece;
         cols = columns;
+        held_for = nullptr;
         const int k = lane % PER * PIECE;
         next = reinterpret_cast<const char*>(p + lane / PER * stride) + k;
         bytes = lane < TILE * PER ? min(max(cols * (int)sizeof(T) - k, 0), PIECE) : 0;
@@ -109,11 +115,13 @@ struct RowCopy {
     template <int BYTES>
     SDM_DEV void small(int first, int left, T* s) const {
         constexpr int E = BYTES / (int)sizeof(T);
-        for (int i = threadIdx.x & 31; i < TILE * W / E; i += 32) {
-            const int r = i * E / W, k = i * E % W;
-            const int n = r < left ? min(max((cols - k) * (int)sizeof(T), 0), BYTES) : 0;
-            copy<BYTES>((uint32_t)__cvta_generic_to_shared(s + i * E),
-                        n ? p + (first + r) * stride + k : p, n);
+        if constexpr (BYTES < PIECE) {
+            for (int i = threadIdx.x & 31; i < TILE * W / E; i += 32) {
+                const int r = i * E / W, k = i * E % W;
+                const int n = r < left ? min(max((cols - k) * (int)sizeof(T), 0), BYTES) : 0;
+                copy<BYTES>((uint32_t)__cvta_generic_to_shared(s + i * E),
+                            n ? p + (first + r) * stride + k : p, n);
+            }
         }
     }
     // The tile that starts `first` tokens behind t0; `left` tokens remain from there.
@@ -132,14 +140,28 @@ struct RowCopy {
             small<8>(first, left, s);
         } else if (piece == 4) {
             small<4>(first, left, s);
-        } else {
-            for (int i = threadIdx.x & 31; i < TILE * W; i += 32) {
-                const int r = i / W, k = i % W;
-                T v = T(0.f);
-                if (r < left && k < cols) v = p[(first + r) * stride + k];
-                s[i] = v;
-            }
+        } else if (HOLD) {
+            load(first, left);
+            held_for = s;
         }
+    }
+    SDM_DEV void load(int first, int left) {
+#pragma unroll
+        for (int j = 0; j < HELD; ++j) {
+            const int i = (threadIdx.x & 31) + 32 * j, r = i / W, k = i % W;
+            held[j] = T(0.f);
+            if (i < TILE * W && r < left && k < cols) held[j] = p[(first + r) * stride + k];
+        }
+    }
+    // Stores what is held.
+    SDM_DEV void flush() {
+        if (!HOLD || !held_for) return;
+#pragma unroll
+        for (int j = 0; j < HELD; ++j) {
+            const int i = (threadIdx.x & 31) + 32 * j;
+            if (i < TILE * W) held_for[i] = held[j];
+        }
+        held_for = nullptr;
     }
 };
 SDM_DEV void async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -259,8 +281,9 @@ struct ScanShared {
 // are computed from what lies there and dropped), so the compiler mixes their arithmetic.
 // Shared memory gives the registers 128 bytes a clock, broadcast or not, which is why a token's
 // step and input are two words and not two pairs.  Registers: 168 let three warps live on a
-// sub-partition; two of eight states a lane do better with more.
-template <typename T, int NPT, int LN, int MODE>
+// sub-partition; two of eight states a lane do better with more.  ODD: some rows are of bf16 at odd
+// addresses.
+template <typename T, int NPT, int LN, int MODE, bool ODD>
 __global__ void __launch_bounds__(32, NPT <= 4 ? 12 : 8) scan_walk_kernel(ScanArgs<T> a) {
     constexpr int NN = NPT * LN, NP = NPT / 2, WCH = 32 / LN;
     constexpr int PAIRS = SCAN_TILE * WCH / 64;  // of (token, channel pair) a lane
@@ -275,8 +298,8 @@ __global__ void __launch_bounds__(32, NPT <= 4 ? 12 : 8) scan_walk_kernel(ScanAr
     const int t0 = blockIdx.y * a.run, t1 = min(t0 + a.run, len);
     if (OUT && t0 >= len && blockIdx.y > 0) return;
     const bool gate = a.z.v.p && (OUT || REV);
-    RowCopy<T, WCH, SCAN_TILE> cu, cd, cz, cg;
-    RowCopy<T, NN, SCAN_TILE> cB, cC;
+    RowCopy<T, WCH, SCAN_TILE, ODD> cu, cd, cz, cg;
+    RowCopy<T, NN, SCAN_TILE, ODD> cB, cC;
     cu.init(a.u, L.b * a.u.v.sb + L.c0, t0, L.cols);
     cd.init(a.delta, L.b * a.delta.v.sb + L.c0, t0, L.cols);
     if (gate) cz.init(a.z, L.b * a.z.v.sb + L.c0, t0, L.cols);
@@ -285,6 +308,14 @@ __global__ void __launch_bounds__(32, NPT <= 4 ? 12 : 8) scan_walk_kernel(ScanAr
     if (OUT || REV) cC.init(a.Cm, L.b * a.Cm.v.sb + L.g * a.Cm.v.sh, t0, a.N);
     auto fetch = [&](int tile) {
         const int first = tile * SCAN_TILE, left = t1 - t0 - first;
+        if (ODD) {  // the tile before it
+            cu.flush();
+            cd.flush();
+            if (gate) cz.flush();
+            if (REV) cg.flush();
+            cB.flush();
+            if (OUT || REV) cC.flush();
+        }
         if (left > 0) {
             auto& s = sh.st[tile % SCAN_STAGES];
             cu.fetch(first, left, s.u);
@@ -492,8 +523,8 @@ __global__ void __launch_bounds__(32, NPT <= 4 ? 12 : 8) scan_walk_kernel(ScanAr
                 row_floats<NPT>(Bs + (q0 + i) * NN, B);
 #pragma unroll
                 for (int p = 0; p < NP; ++p) {
-                    dec[i][p] = pack2(exp2_fast(x.x * A2[2 * p]), exp2_fast(x.x * A2[2 * p + 1]));
-                    in[i][p] = pack2(x.y * B[2 * p], x.y * B[2 * p + 1]);
+                    dec[i][p] = exp2_pair(mul2(dup2(x.x), pack2(A2[2 * p], A2[2 * p + 1])));
+                    in[i][p] = mul2(dup2(x.y), pack2(B[2 * p], B[2 * p + 1]));
                 }
             }
 #pragma unroll

@@ -92,17 +92,23 @@ __global__ void __launch_bounds__(BWD_WARPS * 32, 3) scan_bwd_kernel(ScanBwdArgs
         const int tile = tile_at(k);
         if (k < A.tiles && tile < all && t1 > t0) {
             const int c0 = g * dg + tile * WCH, cols = min(WCH, dg - tile * WCH), p = k & 1;
-            RowCopy<T, WCH, BWD_CHUNK> r;
-            r.init(a.u, b * a.u.v.sb + c0, t0, cols);
-            r.fetch(0, t1 - t0, w.u[p]);
-            r.init(a.delta, b * a.delta.v.sb + c0, t0, cols);
-            r.fetch(0, t1 - t0, w.d[p]);
-            r.init(a.dy, b * a.dy.v.sb + c0, t0, cols);
-            r.fetch(0, t1 - t0, w.dy[p]);
+            constexpr bool ODD = sizeof(T) == 2;
+            RowCopy<T, WCH, BWD_CHUNK, ODD> ru, rd, ry, rz;
+            ru.init(a.u, b * a.u.v.sb + c0, t0, cols);
+            ru.fetch(0, t1 - t0, w.u[p]);
+            rd.init(a.delta, b * a.delta.v.sb + c0, t0, cols);
+            rd.fetch(0, t1 - t0, w.d[p]);
+            ry.init(a.dy, b * a.dy.v.sb + c0, t0, cols);
+            ry.fetch(0, t1 - t0, w.dy[p]);
+            rz.held_for = nullptr;
             if (a.z.v.p) {
-                r.init(a.z, b * a.z.v.sb + c0, t0, cols);
-                r.fetch(0, t1 - t0, w.z[p]);
+                rz.init(a.z, b * a.z.v.sb + c0, t0, cols);
+                rz.fetch(0, t1 - t0, w.z[p]);
             }
+            ru.flush();  // rows at odd addresses: all loaded, then all stored
+            rd.flush();
+            ry.flush();
+            rz.flush();
         }
         async_commit();
     };

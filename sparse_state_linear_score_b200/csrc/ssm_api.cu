@@ -286,14 +286,24 @@ ScanArgs<T> scan_args(const sdm_scan_dims* d, const sdm_view* u, const sdm_view*
     return a;
 }
 
-template <typename T, int NPT, int LN, int MODE>
-sdm_status launch_walk(const ScanArgs<T>& a, int runs, cudaStream_t s) {
+template <typename T, int NPT, int LN, int MODE, bool ODD>
+sdm_status launch_walk_t(const ScanArgs<T>& a, int runs, cudaStream_t s) {
     constexpr int WCH = 32 / LN;
     constexpr size_t smem = sizeof(ScanShared<T, NPT * LN, WCH, MODE>);
-    if (!allow_smem(scan_walk_kernel<T, NPT, LN, MODE>, smem)) return SDM_ERR_CUDA;
+    if (!allow_smem(scan_walk_kernel<T, NPT, LN, MODE, ODD>, smem)) return SDM_ERR_CUDA;
     const unsigned gx = (unsigned)(a.G * ceil_div(a.D / a.G, WCH));
-    scan_walk_kernel<T, NPT, LN, MODE><<<dim3(gx, runs, a.B), 32, smem, s>>>(a);
+    scan_walk_kernel<T, NPT, LN, MODE, ODD><<<dim3(gx, runs, a.B), 32, smem, s>>>(a);
     return launched();
+}
+
+template <typename T, int NPT, int LN, int MODE>
+sdm_status launch_walk(const ScanArgs<T>& a, int runs, cudaStream_t s) {
+    if constexpr (sizeof(T) == 2) {
+        const bool odd = !a.u.piece || !a.delta.piece || (a.z.v.p && !a.z.piece) || !a.Bm.piece ||
+                         !a.Cm.piece || (MODE == SCAN_CHUNK_REV && !a.dy.piece);
+        if (odd) return launch_walk_t<T, NPT, LN, MODE, true>(a, runs, s);
+    }
+    return launch_walk_t<T, NPT, LN, MODE, false>(a, runs, s);
 }
 
 template <typename T, int NPT, int LN>
@@ -494,7 +504,7 @@ NormPlan norm_plan(const sdm_norm_dims* d, bool bwd) {
     return p;
 }
 
-template <bool VEC, bool CL, int DT>
+template <bool VEC, bool CL, int DT, bool ALL>
 sdm_status launch_norm(const NormArgs& a, bool bwd, const NormPlan& p, cudaStream_t s) {
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
@@ -505,26 +515,36 @@ sdm_status launch_norm(const NormArgs& a, bool bwd, const NormPlan& p, cudaStrea
     cfg.stream = s;
     cfg.attrs = &attr;
     cfg.numAttrs = CL ? 1 : 0;
-    const cudaError_t e = bwd ? cudaLaunchKernelEx(&cfg, block_norm_bwd_kernel<VEC, CL, DT>, a)
-                              : cudaLaunchKernelEx(&cfg, block_norm_kernel<VEC, CL, DT>, a);
+    const cudaError_t e = bwd ? cudaLaunchKernelEx(&cfg, block_norm_bwd_kernel<VEC, CL, DT, ALL>, a)
+                              : cudaLaunchKernelEx(&cfg, block_norm_kernel<VEC, CL, DT, ALL>, a);
     (void)cudaGetLastError();
     return e == cudaSuccess ? SDM_OK : SDM_ERR_CUDA;
 }
 
+template <int DT>
+sdm_status launch_norm_typed(const NormArgs& a, bool bwd, const NormPlan& p, cudaStream_t s) {
+    const bool all = a.gate && a.w_post && a.scale && a.w_pre &&
+                     (bwd ? a.dr_out && a.dn && a.dr && a.df && a.dgate : a.r_out && a.n);
+    return all ? launch_norm<true, false, DT, true>(a, bwd, p, s)
+               : launch_norm<true, false, DT, false>(a, bwd, p, s);
+}
+
+// Whole pieces in one block are compiled for their types; wider rows and odd widths look the types
+// up.
 sdm_status launch_norm_any(const NormArgs& a, bool bwd, const NormPlan& p, cudaStream_t s) {
     if (a.D % 4 != 0)
-        return p.blocks > 1 ? launch_norm<false, true, -1>(a, bwd, p, s)
-                            : launch_norm<false, false, -1>(a, bwd, p, s);
-    if (p.blocks > 1) return launch_norm<true, true, -1>(a, bwd, p, s);
+        return p.blocks > 1 ? launch_norm<false, true, -1, false>(a, bwd, p, s)
+                            : launch_norm<false, false, -1, false>(a, bwd, p, s);
+    if (p.blocks > 1) return launch_norm<true, true, -1, false>(a, bwd, p, s);
     switch (a.rb | a.fb << 1 | a.xb << 2) {
-        case 0: return launch_norm<true, false, 0>(a, bwd, p, s);
-        case 1: return launch_norm<true, false, 1>(a, bwd, p, s);
-        case 2: return launch_norm<true, false, 2>(a, bwd, p, s);
-        case 3: return launch_norm<true, false, 3>(a, bwd, p, s);
-        case 4: return launch_norm<true, false, 4>(a, bwd, p, s);
-        case 5: return launch_norm<true, false, 5>(a, bwd, p, s);
-        case 6: return launch_norm<true, false, 6>(a, bwd, p, s);
-        default: return launch_norm<true, false, 7>(a, bwd, p, s);
+        case 0: return launch_norm_typed<0>(a, bwd, p, s);
+        case 1: return launch_norm_typed<1>(a, bwd, p, s);
+        case 2: return launch_norm_typed<2>(a, bwd, p, s);
+        case 3: return launch_norm_typed<3>(a, bwd, p, s);
+        case 4: return launch_norm_typed<4>(a, bwd, p, s);
+        case 5: return launch_norm_typed<5>(a, bwd, p, s);
+        case 6: return launch_norm_typed<6>(a, bwd, p, s);
+        default: return launch_norm_typed<7>(a, bwd, p, s);
     }
 }
 
