@@ -101,16 +101,6 @@ struct RowCopy {
         next = reinterpret_cast<const char*>(p + lane / PER * stride) + k;
         bytes = lane < TILE * PER ? min(max(cols * (int)sizeof(T) - k, 0), PIECE) : 0;
     }
-    template <int BYTES>
-    SDM_DEV static void copy(uint32_t dst, const void* src, int n) {
-        if (BYTES == 16)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
-                         : "memory");
-        else
-            asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src), "r"(n),
-                         "n"(BYTES)
-                         : "memory");
-    }
     // Rows that allow smaller pieces only (or, of bf16 at odd addresses, none).
     template <int BYTES>
     SDM_DEV void small(int first, int left, T* s) const {
@@ -119,8 +109,7 @@ struct RowCopy {
             for (int i = threadIdx.x & 31; i < TILE * W / E; i += 32) {
                 const int r = i * E / W, k = i * E % W;
                 const int n = r < left ? min(max((cols - k) * (int)sizeof(T), 0), BYTES) : 0;
-                copy<BYTES>((uint32_t)__cvta_generic_to_shared(s + i * E),
-                            n ? p + (first + r) * stride + k : p, n);
+                async_copy<BYTES>(s + i * E, n ? p + (first + r) * stride + k : p, n);
             }
         }
     }
@@ -128,12 +117,12 @@ struct RowCopy {
     SDM_DEV void fetch(int first, int left, T* s) {
         if (piece >= PIECE) {
             const int lane = threadIdx.x & 31;
-            const uint32_t dst = (uint32_t)__cvta_generic_to_shared(s) + lane * PIECE;
+            char* dst = reinterpret_cast<char*>(s) + lane * PIECE;
             if (TILE * PER >= 32 || lane < TILE * PER) {
 #pragma unroll
                 for (int i = 0; i < ITER; ++i)
-                    copy<PIECE>(dst + i * 32 * PIECE, next + i * RSTEP * stride * (long long)sizeof(T),
-                                lane / PER + i * RSTEP < left ? bytes : 0);
+                    async_copy<PIECE>(dst + i * 32 * PIECE, next + i * RSTEP * stride * (long long)sizeof(T),
+                                      lane / PER + i * RSTEP < left ? bytes : 0);
             }
             next += TILE * stride * (long long)sizeof(T);
         } else if (piece == 8) {
@@ -155,21 +144,17 @@ struct RowCopy {
     }
     // Stores what is held.
     SDM_DEV void flush() {
-        if (!HOLD || !held_for) return;
+        if constexpr (HOLD) {
+            if (!held_for) return;
 #pragma unroll
-        for (int j = 0; j < HELD; ++j) {
-            const int i = (threadIdx.x & 31) + 32 * j;
-            if (i < TILE * W) held_for[i] = held[j];
+            for (int j = 0; j < HELD; ++j) {
+                const int i = (threadIdx.x & 31) + 32 * j;
+                if (i < TILE * W) held_for[i] = held[j];
+            }
+            held_for = nullptr;
         }
-        held_for = nullptr;
     }
 };
-SDM_DEV void async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-SDM_DEV void async_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // N consecutive floats from shared memory.
 template <int N>
 SDM_DEV void row_floats(const float* p, float (&v)[N]) {

@@ -182,27 +182,41 @@ __global__ void __launch_bounds__(CONV_WARPS * 32) short_conv_kernel(ConvArgs<T>
         for (int k = 0; k < K - 1; ++k) Pairs<V>::store(state + (long long)k * a.d, keep[k]);
     }
 
-    for (int t = t0; t < t1; t += U) {
-        f32x2 cur[U][N];
+    auto walk = [&](auto act) {
+        constexpr bool ACT = decltype(act)::value;
+        for (int t = t0; t < t1; t += U) {
+            f32x2 cur[U][N];
 #pragma unroll
-        for (int i = 0; i < U; ++i) in[i].pairs(cur[i]);
-        fetch(t + U);
+            for (int i = 0; i < U; ++i) in[i].pairs(cur[i]);
+            fetch(t + U);
 #pragma unroll
-        for (int i = 0; i < U; ++i) {
-            f32x2 o[N];
+            for (int i = 0; i < U; ++i) {
+                f32x2 o[N];
 #pragma unroll
-            for (int p = 0; p < N; ++p) {
-                win[K - 1][p] = cur[i][p];
-                o[p] = bias[p];
+                for (int p = 0; p < N; ++p) {
+                    win[K - 1][p] = cur[i][p];
+                    o[p] = bias[p];
 #pragma unroll
-                for (int j = 0; j < K; ++j) o[p] = fma2(w[j][p], win[j][p], o[p]);
+                    for (int j = 0; j < K; ++j) o[p] = fma2(w[j][p], win[j][p], o[p]);
 #pragma unroll
-                for (int j = 0; j < K - 1; ++j) win[j][p] = win[j + 1][p];
-                if (a.act) o[p] = silu2(o[p]);
+                    for (int j = 0; j < K - 1; ++j) win[j][p] = win[j + 1][p];
+                    if (ACT) o[p] = silu2(o[p]);
+                }
+                if (t + i < t1) Pairs<V>::store(y + (t + i) * a.y.st, o);
             }
-            if (t + i < t1) Pairs<V>::store(y + (t + i) * a.y.st, o);
         }
-    }
+    };
+    if (a.act) walk(Flag<true>());
+    else walk(Flag<false>());
+}
+
+// What a lane's loads of the gradient pass through: a ring in shared memory that cp.async fills,
+// three groups of four tokens ahead (whole vectors; each lane reads what it has copied itself), or
+// registers, one group ahead.
+constexpr int CONV_GRP = 4, CONV_RING = 4;
+template <typename T, int V>
+__host__ __device__ constexpr size_t conv_ring_bytes() {
+    return V == 4 ? (size_t)CONV_WARPS * CONV_RING * CONV_GRP * 2 * 32 * V * sizeof(T) : 0;
 }
 
 // A warp takes every (gridDim.y * CONV_WARPS)-th run and sums its share of dw and dbias in
@@ -210,7 +224,9 @@ __global__ void __launch_bounds__(CONV_WARPS * 32) short_conv_kernel(ConvArgs<T>
 // conv_sum_kernel.
 template <typename T, int V, int K>
 __global__ void __launch_bounds__(CONV_WARPS * 32, K <= 4 ? 3 : 1) short_conv_bwd_kernel(ConvArgs<T> a) {
-    constexpr int U = 4, N = Pairs<V>::N;
+    constexpr int U = CONV_GRP, N = Pairs<V>::N;
+    constexpr bool RING = V == 4;
+    extern __shared__ __align__(16) char smem[];
     __shared__ float s_part[CONV_WARPS][K + 1][2 * N][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int nv = a.d / V;
@@ -242,16 +258,21 @@ __global__ void __launch_bounds__(CONV_WARPS * 32, K <= 4 ? 3 : 1) short_conv_bw
         // tokens behind it.  Inputs and g of the last K tokens, oldest first:
         f32x2 win[K][N], g[K][N];
         Raw<T, V> xi[U], gi[U];
+        T* ring = reinterpret_cast<T*>(smem) + (warp * CONV_RING * U * 2 * 32 + lane) * V;
         const int tend = t1 + K - 1, tload = min(tend, len);
-        auto fetch = [&](int t) {
+        // tokens t.. into group k of the ring, or into registers; zero from tload on
+        auto fetch = [&](int k, int t) {
             const T* xp = x + t * a.x.st;
             const T* gp = dy + t * a.dy.st;
-            if (t + U <= tload) {
+            if constexpr (RING) {
+                T* to = ring + k % CONV_RING * U * 2 * 32 * V;
 #pragma unroll
                 for (int i = 0; i < U; ++i) {
-                    xi[i].load(xp + i * a.x.st);
-                    gi[i].load(gp + i * a.dy.st);
+                    const int bytes = t + i < tload ? V * (int)sizeof(T) : 0;
+                    async_copy<V * sizeof(T)>(to + 2 * i * 32 * V, xp + i * a.x.st, bytes);
+                    async_copy<V * sizeof(T)>(to + (2 * i + 1) * 32 * V, gp + i * a.dy.st, bytes);
                 }
+                async_commit();
             } else {
 #pragma unroll
                 for (int i = 0; i < U; ++i) {
@@ -266,15 +287,25 @@ __global__ void __launch_bounds__(CONV_WARPS * 32, K <= 4 ? 3 : 1) short_conv_bw
         };
         // U tokens; EDGE: some of them, or the tokens they complete, lie outside the run, behind
         // the sequence, before its start or in the state after the call.
-        auto group = [&](int t, auto edge) {
-            constexpr bool EDGE = decltype(edge)::value;
+        auto group = [&](int k, int t, auto edge, auto act) {
+            constexpr bool EDGE = decltype(edge)::value, ACT = decltype(act)::value;
             f32x2 cx[U][N], cg[U][N], out[U][N];
+            if constexpr (RING) {
+                async_wait<CONV_RING - 2>();
+                const T* from = ring + k % CONV_RING * U * 2 * 32 * V;
+#pragma unroll
+                for (int i = 0; i < U; ++i) {
+                    xi[i].load(from + 2 * i * 32 * V);
+                    gi[i].load(from + (2 * i + 1) * 32 * V);
+                }
+            }
 #pragma unroll
             for (int i = 0; i < U; ++i) {
                 xi[i].pairs(cx[i]);
                 gi[i].pairs(cg[i]);
             }
-            fetch(t + U);
+            if constexpr (RING) fetch(k + CONV_RING - 1, t + (CONV_RING - 1) * U);
+            else fetch(k + 1, t + U);
 #pragma unroll
             for (int i = 0; i < U; ++i) {
                 const unsigned long long inside = !EDGE || t + i < len ? ~0ull : 0ull;
@@ -283,7 +314,7 @@ __global__ void __launch_bounds__(CONV_WARPS * 32, K <= 4 ? 3 : 1) short_conv_bw
                 for (int p = 0; p < N; ++p) {
                     win[K - 1][p] = cx[i][p];
                     f32x2 gt = cg[i][p];
-                    if (a.act) {
+                    if (ACT) {
                         f32x2 q = bias[p];
 #pragma unroll
                         for (int j = 0; j < K; ++j) q = fma2(w[j][p], win[j][p], q);
@@ -324,17 +355,27 @@ __global__ void __launch_bounds__(CONV_WARPS * 32, K <= 4 ? 3 : 1) short_conv_bw
                 else if (a.dstate) Pairs<V>::store(a.dstate + so + (long long)(s + K - 1) * a.d, out[i]);
             }
         };
-        fetch(t0);
+        if constexpr (RING) {
+#pragma unroll
+            for (int k = 0; k < CONV_RING - 1; ++k) fetch(k, t0 + k * U);
+        } else {
+            fetch(0, t0);
+        }
         conv_load_window<T, V, K>(a, x, state, t0, len, win);
 #pragma unroll
         for (int j = 0; j < K; ++j)
 #pragma unroll
             for (int p = 0; p < N; ++p) g[j][p] = dup2(0.f);
         const int inner = min(t1, len - (K - 1));  // tokens before it are in no state after the call
-        for (int t = t0; t < tend; t += U) {
-            if (t >= t0 + K - 1 && t + U <= inner) group(t, Flag<false>());
-            else group(t, Flag<true>());
-        }
+        auto walk = [&](auto act) {
+            for (int t = t0, k = 0; t < tend; t += U, ++k) {
+                if (t >= t0 + K - 1 && t + U <= inner) group(k, t, Flag<false>(), act);
+                else group(k, t, Flag<true>(), act);
+            }
+        };
+        if (a.act) walk(Flag<true>());
+        else walk(Flag<false>());
+        if (RING) async_wait<0>();  // the next run fills the ring from its start
     }
 #pragma unroll
     for (int p = 0; p < N; ++p) {

@@ -71,9 +71,11 @@ bool vec4_ok(const sdm_view* v, int32_t dtype) {
                   v->st % 4 == 0);
 }
 
+// Dynamic shared memory beyond what a kernel gets unasked: 48 KB, of which these kernels' own arrays
+// take 20 KB at most.
 template <typename K>
 bool allow_smem(K kernel, size_t bytes) {
-    if (bytes <= 48 * 1024) return true;
+    if (bytes <= 28 * 1024) return true;
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) ==
            cudaSuccess;
 }
@@ -108,27 +110,35 @@ ConvPlan conv_plan(const sdm_conv_dims* d, int V) {
     return p;
 }
 
-// The gradient: three blocks an SM, all at once; their shares of dw are added afterwards.
-constexpr int kConvBwdRun = 64;
+// The gradient: runs of 128 tokens (the headline shape takes 88 us, in runs of 64 110 us), shorter
+// ones where those leave SMs without three warps a sub-partition; four blocks an SM, three of them at
+// a time, whose shares of dw are added afterwards.
 ConvPlan conv_bwd_plan(const sdm_conv_dims* d, int V) {
     ConvPlan p;
     p.gx = (unsigned)ceil_div((long long)d->H * (d->d / V), 32);
-    p.run = kConvBwdRun;
+    p.run = 128;
+    while (p.run > 16 && (long long)p.gx * d->B * ceil_div(d->T, p.run) < kSms * 12) p.run /= 2;
     p.runs = (int)std::max(1LL, ceil_div(d->T, p.run));
     const long long need = ceil_div((long long)d->B * p.runs, CONV_WARPS);
-    p.gy = (unsigned)std::max(1LL, std::min(need, 3LL * kSms / p.gx));
+    p.gy = (unsigned)std::max(1LL, std::min(need, 4LL * kSms / p.gx));
     return p;
 }
 
 template <typename T, int V, int K>
-void launch_conv(const ConvArgs<T>& a, const ConvPlan& p, bool bwd, cudaStream_t s) {
+sdm_status launch_conv(const ConvArgs<T>& a, const ConvPlan& p, bool bwd, cudaStream_t s) {
     const dim3 grid(p.gx, p.gy);
-    if (bwd) short_conv_bwd_kernel<T, V, K><<<grid, CONV_WARPS * 32, 0, s>>>(a);
-    else short_conv_kernel<T, V, K><<<grid, CONV_WARPS * 32, 0, s>>>(a);
+    if (bwd) {
+        constexpr size_t ring = conv_ring_bytes<T, V>();
+        if (!allow_smem(short_conv_bwd_kernel<T, V, K>, ring)) return SDM_ERR_CUDA;
+        short_conv_bwd_kernel<T, V, K><<<grid, CONV_WARPS * 32, ring, s>>>(a);
+    } else {
+        short_conv_kernel<T, V, K><<<grid, CONV_WARPS * 32, 0, s>>>(a);
+    }
+    return launched();
 }
 
 template <typename T, int V>
-void launch_conv_k(const ConvArgs<T>& a, const ConvPlan& p, bool bwd, cudaStream_t s) {
+sdm_status launch_conv_k(const ConvArgs<T>& a, const ConvPlan& p, bool bwd, cudaStream_t s) {
     switch (a.K) {
         case 1: return launch_conv<T, V, 1>(a, p, bwd, s);
         case 2: return launch_conv<T, V, 2>(a, p, bwd, s);
@@ -162,9 +172,7 @@ sdm_status run_conv(const sdm_conv_dims* d, const sdm_view* x, const float* w, c
     const bool v4 = d->d % 4 == 0 && vec4_ok(x, d->x_dtype) && vec4_ok(y, d->x_dtype);
     const ConvPlan p = conv_plan(d, v4 ? 4 : 1);
     a.run = p.run, a.runs = p.runs;
-    if (v4) launch_conv_k<T, 4>(a, p, false, s);
-    else launch_conv_k<T, 1>(a, p, false, s);
-    return launched();
+    return v4 ? launch_conv_k<T, 4>(a, p, false, s) : launch_conv_k<T, 1>(a, p, false, s);
 }
 
 template <typename T>
@@ -182,9 +190,7 @@ sdm_status run_conv_bwd(const sdm_conv_dims* d, const sdm_view* x, const float* 
                     vec4_ok(dx, d->x_dtype);
     const ConvPlan p = conv_bwd_plan(d, v4 ? 4 : 1);
     a.run = p.run, a.runs = p.runs;
-    if (v4) launch_conv_k<T, 4>(a, p, true, s);
-    else launch_conv_k<T, 1>(a, p, true, s);
-    const sdm_status e = launched();
+    const sdm_status e = v4 ? launch_conv_k<T, 4>(a, p, true, s) : launch_conv_k<T, 1>(a, p, true, s);
     if (e) return e;
     const long long C = (long long)d->H * d->d;
     conv_sum_kernel<<<(unsigned)ceil_div(C * (d->K + 1), 32), 32 * CSUM_SEG, 0, s>>>(

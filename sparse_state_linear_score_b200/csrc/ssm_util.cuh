@@ -196,6 +196,25 @@ SDM_DEV float softplus(float x) {
     return lo;
 }
 
+// Asynchronous copy of BYTES (4, 8 or 16) to shared memory, of which the first n are read and the
+// rest set to zero.
+template <int BYTES>
+SDM_DEV void async_copy(void* dst, const void* src, int n) {
+    const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
+    if (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(n)
+                     : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(d), "l"(src), "r"(n),
+                     "n"(BYTES)
+                     : "memory");
+}
+SDM_DEV void async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+SDM_DEV void async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 SDM_DEV int clamp_len(const int* lens, int b, int T) {
     if (!lens) return T;
     const int n = lens[b];
