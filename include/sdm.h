@@ -469,14 +469,15 @@ sdm_status sdm_weight_stats(int64_t rows, int32_t K, const float* w, float* cum,
  * contiguous, the other strides free, so that a column slice of a projection is passed without a
  * copy.  A view's data needs only its element's alignment; every other pointer is 16-byte aligned
  * unless a comment says otherwise.  An input stride may be 0 (a broadcast input); negative strides
- * are refused, and an output's rows may not overlap each other (strides of at least a row where
- * the extent is above 1) nor any input.
+ * are refused.  An output's rows may not overlap each other (its strides have to nest: each axis of
+ * more than one entry clears what lies inside it) nor any input, unless a comment says so.  A
+ * workspace may not be shared by calls that can overlap on the GPU.
  *
  * Padded batches: lens [B] int32 (device, or NULL: every sequence has T tokens; 4-byte aligned)
  * are the tokens of each sequence, taken as clamped to [0, T].  Tokens behind them are not read,
  * move no state and leave their output rows as they were; their gradients are written as zero.
  *
- * Sums, states and softmax-free statistics are fp32; each output is rounded once to its type.
+ * Sums, states and the norms' means are fp32; each output is rounded once to its type.
  * Every result is the same from run to run (no atomics: sums over blocks are added in order).
  */
 typedef struct {
@@ -513,7 +514,8 @@ sdm_status sdm_short_conv(const sdm_conv_dims* dims, const sdm_view* x, const fl
  *   dstate_end [B][H][K-1][d] fp32: gradient with respect to the state after the call, or NULL
  *   dx         view [B][H][T][d] x_dtype, written (zero behind lens)
  *   dw [H][d][K], dbias [H][d] fp32, written (dbias may be NULL)
- *   dstate     [B][H][K-1][d] fp32: gradient with respect to the start state, written, or NULL
+ *   dstate     [B][H][K-1][d] fp32: gradient with respect to the start state (also where that is
+ *              the zero of a fresh call), written, or NULL
  *   ws         at least sdm_short_conv_backward_workspace_bytes(dims) bytes
  * Two launches.
  */
@@ -536,7 +538,7 @@ sdm_status sdm_short_conv_backward(const sdm_conv_dims* dims, const sdm_view* x,
  *   state   [B][D][N] fp32, updated in place: read at the start unless dims->fresh is set (then
  *           the start is zero), written at the end.  NULL: start at zero, keep nothing.
  *   ws      at least sdm_selective_scan_workspace_bytes(dims) bytes (may be NULL when that is 0)
- * 1 <= N <= 64; G divides D; B*G <= 65535.  T = 1 is the form for single tokens.  Long calls of
+ * 1 <= N <= 64; G divides D; B*G <= 65535; T <= 2097120.  T = 1 is the form for single tokens.  Long calls of
  * few channels are split over time: one launch, or three.
  */
 typedef struct {
@@ -558,7 +560,8 @@ sdm_status sdm_selective_scan(const sdm_scan_dims* dims, const sdm_view* u, cons
  *                      and the gradient with respect to the state after it (NULL: zero)
  *   du, ddelta, dz     views [B][T][D] of x_dtype, written (dz NULL exactly when z is NULL)
  *   dB, dC             [B][T][G][N] x_dtype, written
- *   dA [D][N]; dDskip, ddt_bias [D] (each may be NULL); dstate [B][D][N] or NULL: fp32, written
+ *   dA [D][N]; dDskip, ddt_bias [D] (each may be NULL); dstate [B][D][N] or NULL (with respect to
+ *                      the start state, also where that is the zero of a fresh call): fp32, written
  *   ws                 at least sdm_selective_scan_backward_workspace_bytes(dims) bytes
  * Up to five launches.
  */
@@ -578,7 +581,7 @@ sdm_status sdm_selective_scan_backward(
  *   p = f / sqrt(mean f^2 + eps) * w_post       (w_post NULL: p = f)
  *   o = r + scale * sigmoid(gate) * p           (scale, gate NULL: 1)
  *   r_out = o,   n = o / sqrt(mean o^2 + eps) * w_pre   (n from o before its rounding)
- *   r, r_out [rows][D] r_dtype (r_out may be r, or NULL); f [rows][D] f_dtype
+ *   r, r_out [rows][D] r_dtype (r_out may be r itself, or NULL); f [rows][D] f_dtype
  *   gate, n  [rows][D] x_dtype (n NULL: r_out only); w_post, scale, w_pre [D] fp32
  * w_pre NULL: n without the weight.  1 <= D <= 16384; eps >= 0.  Rows contiguous.  One launch.
  */

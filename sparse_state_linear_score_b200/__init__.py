@@ -659,7 +659,13 @@ def _elsewhere(f, stream, x, *args):
         raise TypeError(f"{f.__name__} takes CUDA tensors")
     if stream is not None and stream.device != x.device:
         raise ValueError(f"stream is on {stream.device}, the inputs on {x.device}")
-    with torch.cuda.device(x.device) if stream is None else torch.cuda.stream(stream):
+    if stream is None:
+        with torch.cuda.device(x.device):
+            return f(x, *args)
+    for t in (x, *args):  # their memory is not given away while `stream` still uses it
+        if isinstance(t, torch.Tensor) and t.is_cuda:
+            t.record_stream(stream)
+    with torch.cuda.stream(stream):
         return f(x, *args)
 
 
@@ -855,8 +861,7 @@ def _norm_setup(r, f, x_dtype, eps):
 
 
 def block_norm(r, f, w_post=None, gate=None, scale=None, w_pre=None, eps: float = 1e-6,
-               x_dtype=None, r_out=None, n=None,
-               stream=None):
+               x_dtype=None, r_out=None, n=None, stream=None):
     """sdm_block_norm: o = r + scale * sigmoid(gate) * rmsnorm(f) * w_post and n = rmsnorm(o) *
     w_pre over the last dimension of r, f, gate [..., D] -> (r_out like r, n).  r and f are fp32 or
     bf16 each; n has gate's type, or x_dtype (default bfloat16) without a gate.  w_post None: f

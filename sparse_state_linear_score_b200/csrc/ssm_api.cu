@@ -16,7 +16,7 @@ namespace {
 
 constexpr int kSms = 148;
 constexpr int kMaxGrid = 65535;  // of a grid's second and third axis
-constexpr int kScanMaxT = 1 << 21;
+constexpr int kScanMaxT = kMaxGrid * BWD_CHUNK;  // the gradient's chunks are a grid's second axis
 
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }

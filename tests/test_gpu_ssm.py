@@ -159,6 +159,13 @@ SCAN = [  # B, T, D, N, G, dtype, softplus, opt (z, D, dt_bias), lens, view
     (2, 1, 33, 5, 1, "f32", True, False, None, None),
     (2, 1, 20, 33, 2, "f32", True, True, None, None),
     (1, 1, 20, 64, 1, "f32", False, True, None, None),
+    # split over time, sequences that end in the first and in a middle chunk; rows at odd addresses
+    (3, 900, 24, 16, 1, "f32", True, True, [900, 333, 20], None),
+    (2, 700, 9, 11, 1, "bf16", True, True, [95, 700], None),
+    (2, 300, 33, 3, 1, "bf16", True, True, [300, 161], (1, 1)),
+    (1, 260, 6, 1, 3, "bf16", True, False, None, None),
+    (2, 90, 5, 2, 1, "f32", True, True, [64, 32], None),
+    (1, 150, 300, 16, 3, "bf16", True, True, None, (4, 4)),
 ]
 
 
@@ -316,6 +323,8 @@ NORM = [  # rows, D, r, f, x, (w_post, gate, scale, w_pre)
     (2, 16383, "f32", "f32", "f32", (1, 1, 1, 1)),
     (1000, 72, "f32", "f32", "f32", (0, 0, 0, 0)),
     (700, 12, "bf16", "bf16", "f32", (1, 0, 0, 1)),
+    (400, 6001, "bf16", "f32", "bf16", (1, 1, 1, 1)),
+    (200, 12000, "f32", "bf16", "f32", (1, 1, 1, 1)),
 ]
 
 
@@ -491,7 +500,7 @@ def test_streams_and_graphs(sdm):
     c, o, st, dy, _ = scan_case(1, 600, 40, 16, 1, "f32", True, True)
     cg, og = put_scan(c, o, None, None)
     x, w, b, cst, cdy, _, _ = conv_case(1, 2, 30, 16, 4, "f32", "silu", True, None)
-    rr, ff, opt, dro, dn = norm_case(50, 64, "f32", "f32", "f32", (1, 1, 1, 1))
+    rr, ff, opt, dro, dn = norm_case(50, 5000, "f32", "f32", "f32", (1, 1, 1, 1))
     xg, wg, bg, cdyg, dyg = up(x), up(w), up(b), up(cdy), up(dy)
     rg, fg, drog, dng = up(rr), up(ff), up(dro), up(dn)
     optg = {k: up(v) for k, v in opt.items()}
@@ -511,8 +520,13 @@ def test_streams_and_graphs(sdm):
     side.wait_stream(torch.cuda.current_stream())
     y = sdm.selective_scan(*cg.values(), **og, state=hs, stream=side)
     yc = sdm.short_conv(xg, wg, bg, state=cs, stream=side)
+    no, nn = sdm.block_norm(rg, fg, **optg, stream=side)
+    back = [sdm.selective_scan_backward(*cg.values(), dyg, **og, stream=side),
+            sdm.short_conv_backward(xg, wg, cdyg, bg, stream=side),
+            sdm.block_norm_backward(rg, fg, drog, dng, **optg, stream=side)]
     side.synchronize()
-    assert torch.equal(y, want[0]) and torch.equal(yc, want[1]) and torch.equal(hs, want[-2])
+    got = [y, yc, no, nn] + [d[k] for d in back for k in sorted(d)] + [hs, cs]
+    assert len(got) == len(want) and all(torch.equal(a, b2) for a, b2 in zip(got, want))
 
     states = [(st.cuda(), cst.cuda()) for _ in range(2)]
     graphs, outs = [], []
