@@ -8,7 +8,7 @@
 // memory's time.  So the states live in registers over the whole run, NPT a thread, LN
 // neighbouring lanes a channel, and products and multiply-adds go two states at a time (f32x2).
 //
-// A warp works alone, on 32/LN channels of one sequence, in tiles of 16 tokens: cp.async brings the
+// A warp works alone, on 32/LN channels of one sequence, in tiles of 16 or 32 tokens: cp.async brings the
 // next tiles' activations to shared memory; what a token needs once a channel (softplus, before;
 // gate and rounding, after) is spread over all lanes, by token and channel pair; between the two
 // every lane walks the tile's tokens with its states.  One warp a block, so that the SMs get equal
@@ -25,8 +25,17 @@
 namespace sdm {
 namespace ssm {
 
-constexpr int SCAN_TILE = 16;   // tokens staged and walked at a time
-constexpr int SCAN_STAGES = 6;  // tiles in shared memory: three in use, three on their way
+// Tokens staged and walked at a time, and tiles in shared memory: three in use, the others on their
+// way.  Longer tiles pay where a sub-partition has a warp or two of four states a lane (bf16, 1024
+// tokens of 4096 channels: 61 us in tiles of 32, 71 us in tiles of 16; two sequences 86 and 92 us);
+// with eight states a lane they do not fit its registers (133 and 197 us), and rows of fp32 are kept
+// to what lets eight warps live on an SM.
+template <typename T, int NPT>
+struct ScanTile {
+    static constexpr int TILE = NPT <= 4 && sizeof(T) == 2 ? 32 : 16;
+    static constexpr int STAGES = TILE == 32 || (NPT > 4 && sizeof(T) == 4) ? 4 : 6;
+};
+constexpr int SCAN_ROUND = 32;  // chunks are whole tiles of either
 constexpr int SCAN_GRP = 8;     // tokens whose outputs are summed over a channel's lanes together
 enum { SCAN_OUT = 0, SCAN_CHUNK = 1, SCAN_CHUNK_REV = 2 };  // what a walk computes
 
@@ -238,20 +247,21 @@ struct ScanLane {
 };
 
 // A tile in shared memory: u, delta, z, dy [TILE][WCH] and B, C [TILE][NN] as they are stored.
-template <typename T, int NN, int WCH, int MODE>
+template <typename T, int NN, int WCH, int MODE, int TILE>
 struct ScanStage {
-    static constexpr int W = SCAN_TILE * WCH, SPARE = 16 / sizeof(T);
+    static constexpr int W = TILE * WCH, SPARE = 16 / sizeof(T);
     T u[W], d[W], z[MODE == SCAN_CHUNK ? SPARE : W], dy[MODE == SCAN_CHUNK_REV ? W : SPARE];
-    T B[SCAN_TILE * NN], C[SCAN_TILE * NN];
+    T B[TILE * NN], C[TILE * NN];
 };
-template <typename T, int NN, int WCH, int MODE>
+template <typename T, int NPT, int LN, int MODE>
 struct ScanShared {
-    static constexpr int WIDE = sizeof(T) == 2 ? SCAN_TILE * NN : 4;
-    ScanStage<T, NN, WCH, MODE> st[SCAN_STAGES];
+    static constexpr int NN = NPT * LN, WCH = 32 / LN, TILE = ScanTile<T, NPT>::TILE;
+    static constexpr int WIDE = sizeof(T) == 2 ? TILE * NN : 4;
+    ScanStage<T, NN, WCH, MODE, TILE> st[ScanTile<T, NPT>::STAGES];
     float B[WIDE], C[MODE == SCAN_CHUNK ? 4 : WIDE];        // the tile's rows, of bf16
-    float2 tok[SCAN_TILE * WCH];                           // a token's step and step * u
-    float g[MODE == SCAN_CHUNK_REV ? SCAN_TILE * WCH : 4];  // its gated dy
-    float y[MODE == SCAN_OUT ? SCAN_TILE * 32 : 4];         // each lane's share of its sum C h
+    float2 tok[TILE * WCH];                           // a token's step and step * u
+    float g[MODE == SCAN_CHUNK_REV ? TILE * WCH : 4];  // its gated dy
+    float y[MODE == SCAN_OUT ? TILE * 32 : 4];         // each lane's share of its sum C h
 };
 
 // The walk over a chunk.  SCAN_OUT: its outputs from the start state (and the end state where the
@@ -265,17 +275,18 @@ struct ScanShared {
 // nothing in between branches (the flags are masks, the tiles before the first and behind the last
 // are computed from what lies there and dropped), so the compiler mixes their arithmetic.
 // Shared memory gives the registers 128 bytes a clock, broadcast or not, which is why a token's
-// step and input are two words and not two pairs.  Registers: 168 let three warps live on a
-// sub-partition; two of eight states a lane do better with more.  ODD: some rows are of bf16 at odd
+// step and input are two words and not two pairs.  Two warps live on a sub-partition: more registers
+// do better than a third.  ODD: some rows are of bf16 at odd
 // addresses.
 template <typename T, int NPT, int LN, int MODE, bool ODD>
-__global__ void __launch_bounds__(32, NPT <= 4 ? 12 : 8) scan_walk_kernel(ScanArgs<T> a) {
+__global__ void __launch_bounds__(32, 8) scan_walk_kernel(ScanArgs<T> a) {
     constexpr int NN = NPT * LN, NP = NPT / 2, WCH = 32 / LN;
-    constexpr int PAIRS = SCAN_TILE * WCH / 64;  // of (token, channel pair) a lane
+    constexpr int TILE = ScanTile<T, NPT>::TILE, STAGES = ScanTile<T, NPT>::STAGES;
+    constexpr int PAIRS = TILE * WCH / 64;  // of (token, channel pair) a lane
     constexpr int SB = NP >= 8 ? 2 : (NP >= 4 ? 4 : 8);  // tokens whose decays are computed ahead
     constexpr bool OUT = MODE == SCAN_OUT, REV = MODE == SCAN_CHUNK_REV, WIDE = sizeof(T) == 2;
     extern __shared__ __align__(16) char smem[];
-    using Shared = ScanShared<T, NN, WCH, MODE>;
+    using Shared = ScanShared<T, NPT, LN, MODE>;
     Shared& sh = *reinterpret_cast<Shared*>(smem);
     const ScanLane<NPT, LN> L(a.D, a.G);
     const int lane = threadIdx.x;
@@ -283,8 +294,8 @@ __global__ void __launch_bounds__(32, NPT <= 4 ? 12 : 8) scan_walk_kernel(ScanAr
     const int t0 = blockIdx.y * a.run, t1 = min(t0 + a.run, len);
     if (OUT && t0 >= len && blockIdx.y > 0) return;
     const bool gate = a.z.v.p && (OUT || REV);
-    RowCopy<T, WCH, SCAN_TILE, ODD> cu, cd, cz, cg;
-    RowCopy<T, NN, SCAN_TILE, ODD> cB, cC;
+    RowCopy<T, WCH, TILE, ODD> cu, cd, cz, cg;
+    RowCopy<T, NN, TILE, ODD> cB, cC;
     cu.init(a.u, L.b * a.u.v.sb + L.c0, t0, L.cols);
     cd.init(a.delta, L.b * a.delta.v.sb + L.c0, t0, L.cols);
     if (gate) cz.init(a.z, L.b * a.z.v.sb + L.c0, t0, L.cols);
@@ -292,7 +303,7 @@ __global__ void __launch_bounds__(32, NPT <= 4 ? 12 : 8) scan_walk_kernel(ScanAr
     cB.init(a.Bm, L.b * a.Bm.v.sb + L.g * a.Bm.v.sh, t0, a.N);
     if (OUT || REV) cC.init(a.Cm, L.b * a.Cm.v.sb + L.g * a.Cm.v.sh, t0, a.N);
     auto fetch = [&](int tile) {
-        const int first = tile * SCAN_TILE, left = t1 - t0 - first;
+        const int first = tile * TILE, left = t1 - t0 - first;
         if (ODD) {  // the tile before it
             cu.flush();
             cd.flush();
@@ -302,7 +313,7 @@ __global__ void __launch_bounds__(32, NPT <= 4 ? 12 : 8) scan_walk_kernel(ScanAr
             if (OUT || REV) cC.flush();
         }
         if (left > 0) {
-            auto& s = sh.st[tile % SCAN_STAGES];
+            auto& s = sh.st[tile % STAGES];
             cu.fetch(first, left, s.u);
             cd.fetch(first, left, s.d);
             if (gate) cz.fetch(first, left, s.z);
@@ -313,7 +324,7 @@ __global__ void __launch_bounds__(32, NPT <= 4 ? 12 : 8) scan_walk_kernel(ScanAr
         async_commit();
     };
 #pragma unroll 1
-    for (int i = 0; i < SCAN_STAGES - 1; ++i) fetch(i);
+    for (int i = 0; i < STAGES - 1; ++i) fetch(i);
 
     float tmp[NPT], A2[NPT];
     f32x2 h[NP], r[NP], P[NP];
@@ -348,7 +359,7 @@ __global__ void __launch_bounds__(32, NPT <= 4 ? 12 : 8) scan_walk_kernel(ScanAr
     // the steps of a tile: its rows, then its words for the walk
     f32x2 st2[PAIRS], su2[PAIRS], g2[PAIRS];
     auto tile_steps = [&](int tile) {
-        const auto& s = sh.st[tile % SCAN_STAGES];
+        const auto& s = sh.st[tile % STAGES];
         if (!OUT) {
             steps = add2(steps, ahead);
             ahead = dup2(0.f);
@@ -364,7 +375,7 @@ __global__ void __launch_bounds__(32, NPT <= 4 ? 12 : 8) scan_walk_kernel(ScanAr
             st2[k] = add2(pack2(d[0], d[1]), bias);
             const f32x2 sp = softplus2(st2[k]);
             st2[k] = (sp & m_sp) | (st2[k] & ~m_sp);
-            st2[k] &= t0 + tile * SCAN_TILE + e / WCH < t1 ? ~0ull : 0ull;  // else the state stays
+            st2[k] &= t0 + tile * TILE + e / WCH < t1 ? ~0ull : 0ull;  // else the state stays
             su2[k] = mul2(st2[k], pack2(u[0], u[1]));
             if (!OUT) ahead = add2(ahead, st2[k]);
             if (REV) {
@@ -388,7 +399,7 @@ __global__ void __launch_bounds__(32, NPT <= 4 ? 12 : 8) scan_walk_kernel(ScanAr
     // the outputs of a tile whose sums are in sh.y
     f32x2 o2[PAIRS];
     auto tile_outputs = [&](int tile) {
-        const auto& s = sh.st[tile % SCAN_STAGES];
+        const auto& s = sh.st[tile % STAGES];
 #pragma unroll
         for (int k = 0; k < PAIRS; ++k) {
             const int e = 2 * (lane + 32 * k);
@@ -404,7 +415,7 @@ __global__ void __launch_bounds__(32, NPT <= 4 ? 12 : 8) scan_walk_kernel(ScanAr
     auto put_outputs = [&](int tile) {
 #pragma unroll
         for (int k = 0; k < PAIRS; ++k) {
-            const int t = t0 + tile * SCAN_TILE + 2 * (lane + 32 * k) / WCH;
+            const int t = t0 + tile * TILE + 2 * (lane + 32 * k) / WCH;
             if (t >= t0 && t < t1) {
                 float y[2];
                 unpack2(o2[k], y[0], y[1]);
@@ -420,14 +431,14 @@ __global__ void __launch_bounds__(32, NPT <= 4 ? 12 : 8) scan_walk_kernel(ScanAr
     };
 
     // a tile's rows of B and C, of bf16, as floats
-    constexpr int RW = WIDE ? (SCAN_TILE * NN + 255) / 256 : 0;
+    constexpr int RW = WIDE ? (TILE * NN + 255) / 256 : 0;
     float wB[RW + 1][8], wC[RW + 1][8];
     auto wide_rows = [&](int tile) {
         if constexpr (WIDE) {
-            const auto& s = sh.st[tile % SCAN_STAGES];
+            const auto& s = sh.st[tile % STAGES];
 #pragma unroll
             for (int k = 0; k < RW; ++k) {
-                const int e = (lane + 32 * k) * 8 % (SCAN_TILE * NN);  // a small tile: some twice
+                const int e = (lane + 32 * k) * 8 % (TILE * NN);  // a small tile: some twice
                 Vec<8>::load(s.B + e, wB[k]);
                 if (OUT || REV) Vec<8>::load(s.C + e, wC[k]);
             }
@@ -436,7 +447,7 @@ __global__ void __launch_bounds__(32, NPT <= 4 ? 12 : 8) scan_walk_kernel(ScanAr
     auto put_rows = [&]() {
 #pragma unroll
         for (int k = 0; k < RW; ++k) {
-            const int e = (lane + 32 * k) * 8 % (SCAN_TILE * NN);
+            const int e = (lane + 32 * k) * 8 % (TILE * NN);
 #pragma unroll
             for (int i = 0; i < 8; i += 4) {
                 *reinterpret_cast<float4*>(sh.B + e + i) =
@@ -480,26 +491,26 @@ __global__ void __launch_bounds__(32, NPT <= 4 ? 12 : 8) scan_walk_kernel(ScanAr
         }
     };
 
-    const int tiles = max(0, (t1 - t0 + SCAN_TILE - 1) / SCAN_TILE);
+    const int tiles = max(0, (t1 - t0 + TILE - 1) / TILE);
     if (tiles > 0) {
-        async_wait<SCAN_STAGES - 2>();
+        async_wait<STAGES - 2>();
         __syncwarp();
         tile_steps(0);
         wide_rows(0);
         put_steps();
         put_rows();
-        async_wait<SCAN_STAGES - 3>();
+        async_wait<STAGES - 3>();
         __syncwarp();
     }
     for (int tile = 0; tile < tiles; ++tile) {
-        if (OUT) tile_outputs(tile + SCAN_STAGES - 1);  // of the tile before this one
+        if (OUT) tile_outputs(tile + STAGES - 1);  // of the tile before this one
         tile_steps(tile + 1);  // adds this tile's steps to the chunk's
         wide_rows(tile + 1);
-        const float* Bs = (WIDE ? sh.B : reinterpret_cast<const float*>(sh.st[tile % SCAN_STAGES].B)) + L.n0;
-        const float* Cs = (WIDE ? sh.C : reinterpret_cast<const float*>(sh.st[tile % SCAN_STAGES].C)) + L.n0;
-        float y[SCAN_TILE];
+        const float* Bs = (WIDE ? sh.B : reinterpret_cast<const float*>(sh.st[tile % STAGES].B)) + L.n0;
+        const float* Cs = (WIDE ? sh.C : reinterpret_cast<const float*>(sh.st[tile % STAGES].C)) + L.n0;
+        float y[TILE];
 #pragma unroll
-        for (int q0 = 0; q0 < SCAN_TILE; q0 += SB) {
+        for (int q0 = 0; q0 < TILE; q0 += SB) {
             f32x2 dec[SB][NP], in[SB][NP];
 #pragma unroll
             for (int i = 0; i < SB; ++i) {
@@ -540,15 +551,15 @@ __global__ void __launch_bounds__(32, NPT <= 4 ? 12 : 8) scan_walk_kernel(ScanAr
         __syncwarp();  // the tile's words and the outputs' stage have been read
         if (OUT) {
 #pragma unroll
-            for (int q = 0; q < SCAN_TILE; ++q) sh.y[q * 32 + lane] = y[q];
+            for (int q = 0; q < TILE; ++q) sh.y[q * 32 + lane] = y[q];
             put_outputs(tile - 1);
         }
         put_steps();
         put_rows();
-        if (!OUT && (tile + 1) * SCAN_TILE % a.chunk == 0)
-            emit(blockIdx.y * (a.run / a.chunk) + (tile + 1) * SCAN_TILE / a.chunk - 1);
-        fetch(tile + SCAN_STAGES - 1);  // into the stage of the tile before this one
-        async_wait<SCAN_STAGES - 3>();  // the tile after the next is there
+        if (!OUT && (tile + 1) * TILE % a.chunk == 0)
+            emit(blockIdx.y * (a.run / a.chunk) + (tile + 1) * TILE / a.chunk - 1);
+        fetch(tile + STAGES - 1);  // into the stage of the tile before this one
+        async_wait<STAGES - 3>();  // the tile after the next is there
         __syncwarp();
     }
     if (OUT && tiles > 0) {
@@ -556,7 +567,7 @@ __global__ void __launch_bounds__(32, NPT <= 4 ? 12 : 8) scan_walk_kernel(ScanAr
         put_outputs(tiles - 1);
     }
     if (!OUT) {  // the chunks that end behind the last whole one, the empty ones among them
-        const int first = blockIdx.y * (a.run / a.chunk) + tiles * SCAN_TILE / a.chunk;
+        const int first = blockIdx.y * (a.run / a.chunk) + tiles * TILE / a.chunk;
         const int last = min((int)(blockIdx.y + 1) * (a.run / a.chunk), a.nchunk);
         for (int k = first; k < last; ++k) emit(k);
     }

@@ -222,23 +222,39 @@ long long scan_warps(const sdm_scan_dims* d, int LN) {
     return (long long)d->B * d->G * ceil_div(d->D / d->G, 32 / LN);
 }
 
-// Eight states a lane where that makes five warps an SM, else four.  (16 states, bf16, 1024 tokens
-// of 4096 channels: 2 sequences take 95 us in 512 warps of eight a lane and 91 us in 1024 of four,
-// 4 sequences 133 and 177 us; sixteen a lane in one warp of 32 channels 216 us.)  Then chunks of the
-// tokens while half of the SMs' sub-partitions would have no warp: a second pass over the
-// exponentials costs more than it gains above that (at 512 warps 77 us against 70 us).
+// Warps of a walk that live on an SM: eight by their registers, fewer where their tiles are large.
+template <typename T, int NPT>
+long long walk_warps(int LN) {
+    constexpr int TILE = ScanTile<T, NPT>::TILE, STAGES = ScanTile<T, NPT>::STAGES;
+    const size_t es = sizeof(T), ch = 32 / LN, NN = NPT * LN;
+    const size_t rows = TILE * (3 * ch + 2 * NN) * es + 16;
+    const size_t smem = STAGES * rows + (es == 2 ? 2 * TILE * NN * 4 : 0) + TILE * (ch * 8 + 128) + 64;
+    return std::min<long long>(8, 227 * 1024 / (smem + 1024));
+}
+long long walk_warps(const sdm_scan_dims* d, int NPT, int LN) {
+    if (d->x_dtype == SDM_BF16) return NPT == 4 ? walk_warps<bf16, 4>(LN) : walk_warps<bf16, 8>(LN);
+    return NPT == 4 ? walk_warps<float, 4>(LN) : walk_warps<float, 8>(LN);
+}
+
+// Eight states a lane where that makes four warps an SM, else four: eight warps of either live on an
+// SM.  (16 states, bf16, 1024 tokens of 4096 channels: 2 sequences take 95 us in 512 warps of eight
+// a lane and 86 us in 1024 of four, 3 sequences 131 and 139 us, 4 sequences 132 and 169 us; sixteen
+// a lane in one warp of 32 channels 216 us.)  While that leaves half of the SMs' sub-partitions
+// without a warp, chunks of the tokens, eight states a lane: a second pass over the exponentials
+// costs more than it gains above that (at 512 warps 68 us against 61 us).
 ScanPlan scan_plan(const sdm_scan_dims* d) {
     ScanPlan p{};
     p.NN = pad_states(d->N);
-    p.LN = p.NN / 8;
-    if (p.LN < 8 && scan_warps(d, p.LN) < 5 * kSms) p.LN *= 2;
-    const long long warps = scan_warps(d, p.LN);
+    const int eight = p.NN / 8, four = std::min(2 * eight, 8);  // lanes of a channel
     p.chunk = std::max(1, d->T);
     p.nchunk = 1;
-    if (warps <= 2 * kSms) {
-        const long long want = std::min(ceil_div(d->T, 64), 8 * kSms / warps);
+    p.LN = scan_warps(d, eight) < 4 * kSms ? four : eight;
+    if (scan_warps(d, p.LN) <= 2 * kSms) {
+        const long long want = std::min(ceil_div(d->T, 64), walk_warps(d, 8, eight) * kSms /
+                                                                scan_warps(d, eight));
         if (want > 1) {
-            p.chunk = (int)(ceil_div(ceil_div(d->T, want), SCAN_TILE) * SCAN_TILE);
+            p.LN = eight;
+            p.chunk = (int)(ceil_div(ceil_div(d->T, want), SCAN_ROUND) * SCAN_ROUND);
             p.nchunk = (int)ceil_div(d->T, p.chunk);
         }
     }
@@ -295,7 +311,7 @@ ScanArgs<T> scan_args(const sdm_scan_dims* d, const sdm_view* u, const sdm_view*
 template <typename T, int NPT, int LN, int MODE, bool ODD>
 sdm_status launch_walk_t(const ScanArgs<T>& a, int runs, cudaStream_t s) {
     constexpr int WCH = 32 / LN;
-    constexpr size_t smem = sizeof(ScanShared<T, NPT * LN, WCH, MODE>);
+    constexpr size_t smem = sizeof(ScanShared<T, NPT, LN, MODE>);
     if (!allow_smem(scan_walk_kernel<T, NPT, LN, MODE, ODD>, smem)) return SDM_ERR_CUDA;
     const unsigned gx = (unsigned)(a.G * ceil_div(a.D / a.G, WCH));
     scan_walk_kernel<T, NPT, LN, MODE, ODD><<<dim3(gx, runs, a.B), 32, smem, s>>>(a);
