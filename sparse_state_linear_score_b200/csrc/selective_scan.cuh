@@ -164,7 +164,16 @@ struct RowCopy {
         }
     }
 };
-// N consecutive floats from shared memory.
+// N consecutive values from shared memory.
+template <int N>
+SDM_DEV void row_floats(const bf16* p, float (&v)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+        float x[4];
+        Vec<4>::load(p + i, x);
+        v[i] = x[0], v[i + 1] = x[1], v[i + 2] = x[2], v[i + 3] = x[3];
+    }
+}
 template <int N>
 SDM_DEV void row_floats(const float* p, float (&v)[N]) {
 #pragma unroll
@@ -256,9 +265,9 @@ struct ScanStage {
 template <typename T, int NPT, int LN, int MODE>
 struct ScanShared {
     static constexpr int NN = NPT * LN, WCH = 32 / LN, TILE = ScanTile<T, NPT>::TILE;
-    static constexpr int WIDE = sizeof(T) == 2 ? TILE * NN : 4;
+    static constexpr int WIDE = sizeof(T) == 2 && NPT > 4 ? TILE * NN : 4;
     ScanStage<T, NN, WCH, MODE, TILE> st[ScanTile<T, NPT>::STAGES];
-    float B[WIDE], C[MODE == SCAN_CHUNK ? 4 : WIDE];        // the tile's rows, of bf16
+    float B[WIDE], C[MODE == SCAN_CHUNK ? 4 : WIDE];       // the tile's rows, of bf16
     float2 tok[TILE * WCH];                           // a token's step and step * u
     float g[MODE == SCAN_CHUNK_REV ? TILE * WCH : 4];  // its gated dy
     float y[MODE == SCAN_OUT ? TILE * 32 : 4];         // each lane's share of its sum C h
@@ -275,7 +284,10 @@ struct ScanShared {
 // nothing in between branches (the flags are masks, the tiles before the first and behind the last
 // are computed from what lies there and dropped), so the compiler mixes their arithmetic.
 // Shared memory gives the registers 128 bytes a clock, broadcast or not, which is why a token's
-// step and input are two words and not two pairs.  Two warps live on a sub-partition: more registers
+// step and input are two words and not two pairs, and why four states a lane read B and C as bf16
+// (where they are) and convert them in registers (1024 tokens of 4096 channels, two sequences: 80
+// us, as floats 84 us); eight states a lane, which read them half as often, take them as floats that
+// are converted once (130 us, as bf16 138 us).  Two warps live on a sub-partition: more registers
 // do better than a third.  ODD: some rows are of bf16 at odd
 // addresses.
 template <typename T, int NPT, int LN, int MODE, bool ODD>
@@ -284,7 +296,7 @@ __global__ void __launch_bounds__(32, 8) scan_walk_kernel(ScanArgs<T> a) {
     constexpr int TILE = ScanTile<T, NPT>::TILE, STAGES = ScanTile<T, NPT>::STAGES;
     constexpr int PAIRS = TILE * WCH / 64;  // of (token, channel pair) a lane
     constexpr int SB = NP >= 8 ? 2 : (NP >= 4 ? 4 : 8);  // tokens whose decays are computed ahead
-    constexpr bool OUT = MODE == SCAN_OUT, REV = MODE == SCAN_CHUNK_REV, WIDE = sizeof(T) == 2;
+    constexpr bool OUT = MODE == SCAN_OUT, REV = MODE == SCAN_CHUNK_REV, WIDE = sizeof(T) == 2 && NPT > 4;
     extern __shared__ __align__(16) char smem[];
     using Shared = ScanShared<T, NPT, LN, MODE>;
     Shared& sh = *reinterpret_cast<Shared*>(smem);
@@ -430,6 +442,15 @@ __global__ void __launch_bounds__(32, 8) scan_walk_kernel(ScanArgs<T> a) {
         }
     };
 
+    // where the walk finds a tile's rows of B and C
+    auto rows_B = [&](int tile) {
+        if constexpr (WIDE) return static_cast<const float*>(sh.B);
+        else return static_cast<const T*>(sh.st[tile % STAGES].B);
+    };
+    auto rows_C = [&](int tile) {
+        if constexpr (WIDE) return static_cast<const float*>(sh.C);
+        else return static_cast<const T*>(sh.st[tile % STAGES].C);
+    };
     // a tile's rows of B and C, of bf16, as floats
     constexpr int RW = WIDE ? (TILE * NN + 255) / 256 : 0;
     float wB[RW + 1][8], wC[RW + 1][8];
@@ -506,8 +527,8 @@ __global__ void __launch_bounds__(32, 8) scan_walk_kernel(ScanArgs<T> a) {
         if (OUT) tile_outputs(tile + STAGES - 1);  // of the tile before this one
         tile_steps(tile + 1);  // adds this tile's steps to the chunk's
         wide_rows(tile + 1);
-        const float* Bs = (WIDE ? sh.B : reinterpret_cast<const float*>(sh.st[tile % STAGES].B)) + L.n0;
-        const float* Cs = (WIDE ? sh.C : reinterpret_cast<const float*>(sh.st[tile % STAGES].C)) + L.n0;
+        const auto* Bs = rows_B(tile) + L.n0;
+        const auto* Cs = rows_C(tile) + L.n0;
         float y[TILE];
 #pragma unroll
         for (int q0 = 0; q0 < TILE; q0 += SB) {

@@ -228,7 +228,7 @@ long long walk_warps(int LN) {
     constexpr int TILE = ScanTile<T, NPT>::TILE, STAGES = ScanTile<T, NPT>::STAGES;
     const size_t es = sizeof(T), ch = 32 / LN, NN = NPT * LN;
     const size_t rows = TILE * (3 * ch + 2 * NN) * es + 16;
-    const size_t smem = STAGES * rows + (es == 2 ? 2 * TILE * NN * 4 : 0) + TILE * (ch * 8 + 128) + 64;
+    const size_t smem = STAGES * rows + (es == 2 && NPT > 4 ? 2 * TILE * NN * 4 : 0) + TILE * (ch * 8 + 128) + 64;
     return std::min<long long>(8, 227 * 1024 / (smem + 1024));
 }
 long long walk_warps(const sdm_scan_dims* d, int NPT, int LN) {
@@ -238,7 +238,7 @@ long long walk_warps(const sdm_scan_dims* d, int NPT, int LN) {
 
 // Eight states a lane where that makes four warps an SM, else four: eight warps of either live on an
 // SM.  (16 states, bf16, 1024 tokens of 4096 channels: 2 sequences take 95 us in 512 warps of eight
-// a lane and 86 us in 1024 of four, 3 sequences 131 and 139 us, 4 sequences 132 and 169 us; sixteen
+// a lane and 80 us in 1024 of four, 3 sequences 131 and 139 us, 4 sequences 132 and 169 us; sixteen
 // a lane in one warp of 32 channels 216 us.)  While that leaves half of the SMs' sub-partitions
 // without a warp, chunks of the tokens, eight states a lane: a second pass over the exponentials
 // costs more than it gains above that (at 512 warps 68 us against 61 us).
