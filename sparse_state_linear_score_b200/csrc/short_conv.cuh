@@ -42,35 +42,7 @@ struct Flag {
     static constexpr bool value = B;
 };
 
-// V channels of a token as they are stored: what a load in flight leaves in registers, so that
-// nothing waits for it before its values are used.
-template <typename T, int V>
-struct Raw;
-template <>
-struct Raw<float, 4> {
-    float4 x;
-    SDM_DEV void clear() { x = make_float4(0.f, 0.f, 0.f, 0.f); }
-    SDM_DEV void load(const float* p) { x = *reinterpret_cast<const float4*>(p); }
-    SDM_DEV void pairs(f32x2 (&v)[2]) const { v[0] = pack2(x.x, x.y), v[1] = pack2(x.z, x.w); }
-};
-template <>
-struct Raw<bf16, 4> {
-    uint2 x;
-    SDM_DEV void clear() { x = make_uint2(0u, 0u); }
-    SDM_DEV void load(const bf16* p) { x = *reinterpret_cast<const uint2*>(p); }
-    SDM_DEV void pairs(f32x2 (&v)[2]) const {
-        v[0] = pack2(bf16_lo(x.x), bf16_hi(x.x)), v[1] = pack2(bf16_lo(x.y), bf16_hi(x.y));
-    }
-};
-template <typename T>
-struct Raw<T, 1> {
-    T x;
-    SDM_DEV void clear() { x = T(0.f); }
-    SDM_DEV void load(const T* p) { x = *p; }
-    SDM_DEV void pairs(f32x2 (&v)[1]) const { v[0] = pack2(ld(&x), 0.f); }
-};
-
-// The same as pairs of floats (one channel: a pair with a zero).
+// V channels of a token as pairs of floats (one channel: a pair with a zero).
 template <int V>
 struct Pairs {
     static constexpr int N = (V + 1) / 2;

@@ -154,6 +154,47 @@ SDM_DEV float max_nan(float a, float b) {
     return r;
 }
 
+// V consecutive values as they are stored: what a load in flight leaves in registers, so that
+// nothing waits for it before they are used.
+template <typename T, int V>
+struct Raw;
+template <>
+struct Raw<float, 4> {
+    float4 x;
+    SDM_DEV void clear() { x = make_float4(0.f, 0.f, 0.f, 0.f); }
+    SDM_DEV void load(const float* p) { x = *reinterpret_cast<const float4*>(p); }
+    SDM_DEV void load(const float* p, int cnt) {  // the first cnt, where p is not aligned to four
+        if (cnt > 0) x.x = p[0];
+        if (cnt > 1) x.y = p[1];
+        if (cnt > 2) x.z = p[2];
+        if (cnt > 3) x.w = p[3];
+    }
+    SDM_DEV void pairs(f32x2 (&v)[2]) const { v[0] = pack2(x.x, x.y), v[1] = pack2(x.z, x.w); }
+};
+template <>
+struct Raw<bf16, 4> {
+    uint2 x;
+    SDM_DEV void clear() { x = make_uint2(0u, 0u); }
+    SDM_DEV void load(const bf16* p) { x = *reinterpret_cast<const uint2*>(p); }
+    SDM_DEV void load(const bf16* p, int cnt) {
+        const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
+        if (cnt > 0) x.x = q[0];
+        if (cnt > 1) x.x |= (uint32_t)q[1] << 16;
+        if (cnt > 2) x.y = q[2];
+        if (cnt > 3) x.y |= (uint32_t)q[3] << 16;
+    }
+    SDM_DEV void pairs(f32x2 (&v)[2]) const {
+        v[0] = pack2(bf16_lo(x.x), bf16_hi(x.x)), v[1] = pack2(bf16_lo(x.y), bf16_hi(x.y));
+    }
+};
+template <typename T>
+struct Raw<T, 1> {
+    T x;
+    SDM_DEV void clear() { x = T(0.f); }
+    SDM_DEV void load(const T* p) { x = *p; }
+    SDM_DEV void pairs(f32x2 (&v)[1]) const { v[0] = pack2(ld(&x), 0.f); }
+};
+
 // x sigmoid(x) of two values.  Below -126 ln 2 the exponential passes rcp's range: the result is
 // then 0 where it is above -2^-118.
 SDM_DEV f32x2 silu2(f32x2 x) {

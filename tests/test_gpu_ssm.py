@@ -159,6 +159,9 @@ SCAN = [  # B, T, D, N, G, dtype, softplus, opt (z, D, dt_bias), lens, view
     (2, 1, 33, 5, 1, "f32", True, False, None, None),
     (2, 1, 20, 33, 2, "f32", True, True, None, None),
     (1, 1, 20, 64, 1, "f32", False, True, None, None),
+    # four sequences a thread, the last ones missing
+    (13, 1, 9600, 16, 1, "bf16", True, True, [1, 0, 1, 1, 1, 1, 0, 0, 1, 1, 1, 1, 0], None),
+    (14, 1, 20000, 7, 2, "f32", True, True, None, None),
     # split over time, sequences that end in the first and in a middle chunk; rows at odd addresses
     (3, 900, 24, 16, 1, "f32", True, True, [900, 333, 20], None),
     (2, 700, 9, 11, 1, "bf16", True, True, [95, 700], None),
