@@ -14,6 +14,9 @@
  *   sdm_forward      the sparse gated-delta recurrence over T tokens (prefill)
  *   sdm_decode_step  one token per sequence (scoring + recurrence)
  *
+ * and, below, the operators of a state-space block beside it: sdm_short_conv,
+ * sdm_selective_scan and sdm_block_norm, with their gradients.
+ *
  * Notation: B sequences, H heads, T tokens, key width d_k (two halves of
  * h = d_k/2), n sub-keys per half (N = n*n slots, slot s = i*n + j where i is
  * the rank source of the first half), value width d_v, per-half top-k k_half,
@@ -410,7 +413,7 @@ sdm_status sdm_gemm_bf16(int32_t M, int32_t N, int32_t K, const void* A, const v
  *   q, k  [B][H][T][d_k] bf16 (dims->x_dtype must be bf16); v [B][H][T][d_v] (v_dtype)
  *   g     [B][T][H*d_v] bf16 (for sdm_layer_out); alpha, beta [B][H][T] fp32
  *   ws    at least sdm_layer_in_workspace_bytes(dims) bytes (P, fp32)
- * No short convolution and no q/k normalisation.  Two launches.
+ * No short convolution (sdm_short_conv takes q, k and v) and no q/k normalisation.  Two launches.
  */
 size_t sdm_layer_in_workspace_bytes(const sdm_dims* dims);
 sdm_status sdm_layer_in(const sdm_dims* dims, const void* x, const void* Win_t,

@@ -18,6 +18,10 @@
 // chunk is exp(A sum s), so a chunk's effect on the state is its end state from zero and the sum
 // of its steps.  The same walk computes those first (the exponentials once more),
 // scan_carry_kernel chains them, and every chunk's outputs start from its true state.
+//
+// Measured, 16 states: 2 sequences of 4096 tokens, 4096 channels, bf16, 271 us (119 us of
+// exponentials; issue 60 %, exponential unit 54 %, shared memory 57 %, 1.7 warps a sub-partition);
+// one of 16384 tokens, 512 channels, fp32, 113 us in 37 chunks.
 #pragma once
 
 #include "ssm_util.cuh"
@@ -603,7 +607,8 @@ __global__ void __launch_bounds__(32, 8) scan_walk_kernel(ScanArgs<T> a) {
 
 // Chains the chunks: E[k] becomes the state that chunk k starts from and, in the gradient (the
 // grid's second row), R[k] the carry that reaches its last token.  One thread a state; the loads of
-// SCAN_AHEAD chunks are in flight together.  Bound by memory.
+// SCAN_AHEAD chunks are in flight together.  Bound by memory: both directions of 2 x 64 chunks of
+// 2048 x 16 states, 67 MB read and 67 MB written, take 20 us.
 constexpr int SCAN_AHEAD = 8;
 template <typename T>
 __global__ void __launch_bounds__(256) scan_carry_kernel(ScanArgs<T> a) {

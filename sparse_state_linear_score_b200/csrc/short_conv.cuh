@@ -4,12 +4,14 @@
 //   g_t  = dy_t act'(p_t),   dx_s = sum_j w[j] g_{s+K-1-j} (+ dstate_end where s is kept),
 //   dw_j = sum_{b,t} g_t x_{t-K+1+j},  dbias = sum_{b,t} g_t
 //
-// Bound by memory: 2 reads or writes an element (forward), 3 (backward), about 2K + 5 (6K + 8)
-// operations.  A warp walks a run of tokens of one sequence; its lanes hold 32 neighbouring
-// channel vectors of the flattened (head, channel) axis, whose filters stay in registers, and
-// the last K-1 tokens move through a register window, so each input is read from memory once
-// (plus K-1 tokens where runs meet, which L2 holds).  The loads of the next tokens are issued
-// before the current ones are used.
+// Bound by memory: 2 reads or writes an element (forward), 3 (gradient), about 2K + 5 (6K + 8)
+// operations.  A warp walks a run of tokens of one sequence; its lanes hold 32 neighbouring vectors
+// of the flattened (head, channel) axis, whose filters stay in registers, and the last K-1 tokens
+// move through a register window, so each input is read from memory once (plus K-1 tokens where
+// runs meet, which L2 holds).  Loads are issued as they are stored and converted only when used: a
+// conversion behind a load waits for it (the gradient took 506 us so, 206 us without).
+// Measured, bf16, K = 4, caches cold: forward 2 x 4 x 4096 x 128 9.7 us; gradient 8 x 16 x 8192 x 64
+// 88 us, 4.3 TB/s, 55 % of the issue slots.
 #pragma once
 
 #include "ssm_util.cuh"
