@@ -168,6 +168,7 @@ struct RowCopy {
         }
     }
 };
+
 // N consecutive values from shared memory.
 template <int N>
 SDM_DEV void row_floats(const bf16* p, float (&v)[N]) {
@@ -224,17 +225,14 @@ struct ScanLane {
         n0 = nl * NPT;
         b = blockIdx.z;
     }
-    static constexpr int PC = NPT < 4 ? NPT : 4;
     SDM_DEV void load(const float* p, int N, float (&v)[NPT]) const {  // p: the channel's row
-        if (N % 4 == 0) {  // rows of whole pieces
+        if (N % 4 == 0) {  // rows of whole 16-byte pieces
 #pragma unroll
-            for (int i = 0; i < NPT; i += PC) {
-                float x[PC];
+            for (int i = 0; i < NPT; i += 4) {
+                float x[4] = {0.f, 0.f, 0.f, 0.f};
+                if (live && n0 + i < N) Vec<4>::load(p + n0 + i, x);
 #pragma unroll
-                for (int k = 0; k < PC; ++k) x[k] = 0.f;
-                if (live && n0 + i < N) Vec<PC>::load(p + n0 + i, x);
-#pragma unroll
-                for (int k = 0; k < PC; ++k) v[i + k] = x[k];
+                for (int k = 0; k < 4; ++k) v[i + k] = x[k];
             }
         } else {
 #pragma unroll
@@ -245,11 +243,9 @@ struct ScanLane {
         if (!live) return;
         if (N % 4 == 0) {
 #pragma unroll
-            for (int i = 0; i < NPT; i += PC) {
-                float x[PC];
-#pragma unroll
-                for (int k = 0; k < PC; ++k) x[k] = v[i + k];
-                if (n0 + i < N) Vec<PC>::store(p + n0 + i, x);
+            for (int i = 0; i < NPT; i += 4) {
+                const float x[4] = {v[i], v[i + 1], v[i + 2], v[i + 3]};
+                if (n0 + i < N) Vec<4>::store(p + n0 + i, x);
             }
         } else {
 #pragma unroll
@@ -271,8 +267,8 @@ struct ScanShared {
     static constexpr int NN = NPT * LN, WCH = 32 / LN, TILE = ScanTile<T, NPT>::TILE;
     static constexpr int WIDE = sizeof(T) == 2 && NPT > 4 ? TILE * NN : 4;
     ScanStage<T, NN, WCH, MODE, TILE> st[ScanTile<T, NPT>::STAGES];
-    float B[WIDE], C[MODE == SCAN_CHUNK ? 4 : WIDE];       // the tile's rows, of bf16
-    float2 tok[TILE * WCH];                           // a token's step and step * u
+    float B[WIDE], C[MODE == SCAN_CHUNK ? 4 : WIDE];   // the tile's rows, of bf16
+    float2 tok[TILE * WCH];                            // a token's step and step * u
     float g[MODE == SCAN_CHUNK_REV ? TILE * WCH : 4];  // its gated dy
     float y[MODE == SCAN_OUT ? TILE * 32 : 4];         // each lane's share of its sum C h
 };
@@ -292,14 +288,13 @@ struct ScanShared {
 // (where they are) and convert them in registers (1024 tokens of 4096 channels, two sequences: 80
 // us, as floats 84 us); eight states a lane, which read them half as often, take them as floats that
 // are converted once (130 us, as bf16 138 us).  Two warps live on a sub-partition: more registers
-// do better than a third.  ODD: some rows are of bf16 at odd
-// addresses.
+// do better than a third.  ODD: some rows are of bf16 at odd addresses.
 template <typename T, int NPT, int LN, int MODE, bool ODD>
 __global__ void __launch_bounds__(32, 8) scan_walk_kernel(ScanArgs<T> a) {
     constexpr int NN = NPT * LN, NP = NPT / 2, WCH = 32 / LN;
     constexpr int TILE = ScanTile<T, NPT>::TILE, STAGES = ScanTile<T, NPT>::STAGES;
     constexpr int PAIRS = TILE * WCH / 64;  // of (token, channel pair) a lane
-    constexpr int SB = NP >= 8 ? 2 : (NP >= 4 ? 4 : 8);  // tokens whose decays are computed ahead
+    constexpr int SB = NP >= 4 ? 4 : 8;      // tokens whose decays are computed ahead
     constexpr bool OUT = MODE == SCAN_OUT, REV = MODE == SCAN_CHUNK_REV, WIDE = sizeof(T) == 2 && NPT > 4;
     extern __shared__ __align__(16) char smem[];
     using Shared = ScanShared<T, NPT, LN, MODE>;
@@ -652,11 +647,12 @@ __global__ void __launch_bounds__(256) scan_carry_kernel(ScanArgs<T> a) {
     }
 }
 
-// One token a sequence: bound by the state, read and written once (8 N bytes a channel against
-// 8 of activations in bf16; 64 sequences of 4096 channels of 16 states, 36 MB, take 13.4 us with
-// cold caches, 2.7 TB/s, of which about 3 us are the launch).  Four states a thread, so that a warp's state accesses are whole
-// contiguous lines, of NB sequences, whose loads are all in flight before the first is used and share
-// the channel's A, bias and addresses.  vec: B and C can be read four at a time.
+// One token a sequence: bound by the state, read and written once (8 N bytes a channel against 8 of
+// activations in bf16; 64 sequences of 4096 channels of 16 states, 36 MB, take 13.4 us with cold
+// caches, 2.7 TB/s, of which about 3 us are the launch).  Four states a thread, so that a warp's
+// state accesses are whole contiguous lines, of NB sequences, whose loads are all in flight before
+// the first is used and share the channel's A, bias and addresses.  vec: B and C can be read four at
+// a time.
 template <typename T, int LN, int NB>
 __global__ void __launch_bounds__(256) scan_step_kernel(ScanArgs<T> a, bool vec) {
     const int nl = threadIdx.x % LN, n0 = nl * 4;

@@ -331,11 +331,13 @@ sdm_status launch_walk(const ScanArgs<T>& a, int runs, cudaStream_t s) {
 template <typename T, int NPT, int LN>
 sdm_status launch_scan_t(ScanArgs<T> a, const sdm_view* const (&v)[6], cudaStream_t s) {
     set_pieces(a, v, 32 / LN, NPT * LN);
-    if (a.nchunk > 1) {
-        const sdm_status e = launch_walk<T, NPT, LN, SCAN_CHUNK>(a, a.nchunk - 1, s);
-        if (e) return e;
-        const long long n = (long long)a.B * a.D * a.N;
-        scan_carry_kernel<T><<<(unsigned)ceil_div(n, 256), 256, 0, s>>>(a);
+    if constexpr (NPT == 8) {  // four states a lane are not split over time
+        if (a.nchunk > 1) {
+            const sdm_status e = launch_walk<T, NPT, LN, SCAN_CHUNK>(a, a.nchunk - 1, s);
+            if (e) return e;
+            const long long n = (long long)a.B * a.D * a.N;
+            scan_carry_kernel<T><<<(unsigned)ceil_div(n, 256), 256, 0, s>>>(a);
+        }
     }
     return launch_walk<T, NPT, LN, SCAN_OUT>(a, a.nchunk, s);
 }
@@ -373,7 +375,7 @@ sdm_status run_scan(const sdm_scan_dims* d, ScanArgs<T> a, const sdm_view* const
     a.chunk = a.run = p.chunk, a.nchunk = p.nchunk;
     a.E = static_cast<float*>(ws);
     a.S = reinterpret_cast<float*>(static_cast<char*>(ws) + p.off_S);
-    if (p.LN * 8 == p.NN) {
+    if (p.LN * 8 == p.NN) {  // eight states a lane
         switch (p.LN) {
             case 1: return launch_scan_t<T, 8, 1>(a, v, s);
             case 2: return launch_scan_t<T, 8, 2>(a, v, s);
