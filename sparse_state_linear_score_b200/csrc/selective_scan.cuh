@@ -342,7 +342,7 @@ __global__ void __launch_bounds__(32, 8) scan_walk_kernel(ScanArgs<T> a) {
     L.load(a.A + (long long)L.c * a.N, a.N, A2);
 #pragma unroll
     for (int i = 0; i < NPT; ++i) {
-        A2[i] *= kLog2e;
+        A2[i] = decay_rate(A2[i]);
         tmp[i] = 0.f;
     }
     const long long at = ((long long)L.b * a.nchunk + blockIdx.y) * a.D + L.c;
@@ -612,7 +612,7 @@ __global__ void __launch_bounds__(256) scan_carry_kernel(ScanArgs<T> a) {
     const long long dn = (long long)a.D * a.N;
     if (i >= a.B * dn) return;
     const long long b = i / dn, cn = i % dn;
-    const float A2 = a.A[cn] * kLog2e;
+    const float A2 = decay_rate(a.A[cn]);
     const long long last = a.nchunk - 1;
     const long long step = rev ? -1 : 1;
     float* E = (rev ? a.R : a.E) + (b * a.nchunk + (rev ? last : 0)) * dn + cn;
@@ -706,7 +706,11 @@ __global__ void __launch_bounds__(256) scan_step_kernel(ScanArgs<T> a, bool vec)
     load4(a.A + (long long)cc * a.N + n0, A2);
     const float bias = a.dt_bias ? a.dt_bias[cc] : 0.f, skip = a.Dskip ? a.Dskip[cc] : 0.f;
 #pragma unroll
-    for (int r = 0; r < 2; ++r) A2[r] = mul2(A2[r], dup2(kLog2e));
+    for (int r = 0; r < 2; ++r) {
+        float lo, hi;
+        unpack2(A2[r], lo, hi);
+        A2[r] = pack2(decay_rate(lo), decay_rate(hi));
+    }
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
         const int b = b0 + j;

@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(BWD_WARPS * 32, 3) scan_bwd_kernel(ScanBwdArgs
             }
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                A2[i] = pack2(av[2 * i] * kLog2e, av[2 * i + 1] * kLog2e);
+                A2[i] = pack2(decay_rate(av[2 * i]), decay_rate(av[2 * i + 1]));
                 h[i] = pack2(hv[2 * i], hv[2 * i + 1]);
                 gr[i] = pack2(gv[2 * i], gv[2 * i + 1]);
                 dA[i] = zero;

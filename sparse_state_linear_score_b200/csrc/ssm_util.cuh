@@ -154,6 +154,11 @@ SDM_DEV float max_nan(float a, float b) {
     return r;
 }
 
+// A state's rate for exp2(s * rate) = e^(s A).  Kept finite where A log2(e) is not (A of the type's
+// lowest value, or -inf where -e^x overflowed): a step of zero, also that of a row behind the
+// sequence, then leaves the state as it is instead of making it 0 * inf.
+SDM_DEV float decay_rate(float A) { return max_nan(A * kLog2e, -3.402823466e38f); }
+
 // V consecutive values as they are stored: what a load in flight leaves in registers, so that
 // nothing waits for it before they are used.
 template <typename T, int V>

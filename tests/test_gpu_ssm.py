@@ -299,6 +299,35 @@ def test_scan_extreme_steps(sdm):
     R.within(y, ref, mag + 1e-30, 6 * T + 128, "y")
 
 
+@pytest.mark.parametrize("B,T,lens", [(3, 37, [37, 20, 0]), (2, 300, [300, 161]), (3, 1, [1, 0, 1])])
+def test_scan_infinite_rates_and_masked_tokens(sdm, B, T, lens):
+    """A of -inf or of the type's lowest value forgets at every token, and rows behind a sequence
+    still leave its state; tokens masked by a delta of -inf or of the lowest value are passed over."""
+    D, N, low = 8, 16, torch.finfo(torch.float32).min
+    c, o, st, dy, de = scan_case(B, T, D, N, 1, "f32", True, True)
+    c["A"][1], c["A"][2], c["A"][3, ::2] = -float("inf"), low, -float("inf")
+    c["delta"][:, ::3, 4], c["delta"][:, ::4, 5] = -float("inf"), low
+    ln = torch.tensor(lens, dtype=torch.int32).cuda()
+    cg, og = put_scan(c, o, lens, None)
+    stg = st.cuda()
+    y = sdm.selective_scan(*cg.values(), **og, state=stg, lens=ln)
+    (ref, end), (mag, mend) = scan_ref(c, o, st, lens, True), scan_ref(c, o, st, lens, True, True)
+    n = 6 * T + 64 + N
+    R.within(stg, end, mend + 1e-30, n, "state")
+    R.within(y, ref, mag + 1e-30, n + 64, "y")
+    # the gradient's formula has A q: finite for the lowest value, 0 * inf for -inf
+    c["A"].clamp_(min=low)
+    cg["A"] = c["A"].cuda()
+    g = sdm.selective_scan_backward(*cg.values(), poison(dy, lens, 1).cuda(), **og, state=up(st),
+                                    lens=ln, dstate_end=up(de))
+    a = [c[k].double() for k in ("u", "delta", "A", "B", "C")] + [dy.double()] + \
+        [d64(o[k]) for k in ("D", "z", "dt_bias")] + [st.double(), lens, True, de.double()]
+    ref, mag = R.scan_bwd(*a), R.scan_bwd(*a, mag=True)
+    for k in sorted(ref):
+        m = 12 * T + 200 + N + D + (B * T if k in ("dA", "dD", "ddt_bias") else 0)
+        R.within(g[k], ref[k], mag[k] + 1e-30, m, k)
+
+
 def test_scan_outputs_are_reproducible(sdm):
     c, o, st, dy, de = scan_case(2, 300, 200, 16, 2, "bf16", True, True)
     cg, og = put_scan(c, o, None, None)
