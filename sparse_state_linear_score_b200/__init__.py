@@ -688,12 +688,21 @@ def _scratch(ws, nbytes, like):
     return ws, _ptr(ws, "ws"), ws.numel() * ws.element_size()
 
 
+def _sized(struct, sizes):
+    """A dims structure; ctypes would cut a size that its field does not hold."""
+    c = struct(*sizes)
+    for (name, kind), v in zip(struct._fields_, sizes):
+        if kind is not ctypes.c_float and getattr(c, name) != v:
+            raise ValueError(f"{name} = {v} is too large")
+    return c
+
+
 _ACT = {None: 0, "none": 0, "silu": 1}
 
 
 @functools.lru_cache(maxsize=1024)
 def _conv_dims(*sizes):
-    c = _ConvDims(*sizes)
+    c = _sized(_ConvDims, sizes)
     return c, _lib.sdm_short_conv_backward_workspace_bytes(ctypes.byref(c))
 
 
@@ -763,7 +772,7 @@ def short_conv_backward(x, w, dy, bias=None, act="silu", state=None, lens=None, 
 
 @functools.lru_cache(maxsize=1024)
 def _scan_dims(*sizes):
-    c = _ScanDims(*sizes)
+    c = _sized(_ScanDims, sizes)
     return c, _lib.sdm_selective_scan_workspace_bytes(ctypes.byref(c)), \
         _lib.sdm_selective_scan_backward_workspace_bytes(ctypes.byref(c))
 
@@ -848,7 +857,7 @@ def selective_scan_backward(u, delta, A, B, C, dy, D=None, z=None, dt_bias=None,
 
 @functools.lru_cache(maxsize=1024)
 def _norm_dims(*sizes):
-    c = _NormDims(*sizes)
+    c = _sized(_NormDims, sizes)
     return c, _lib.sdm_block_norm_backward_workspace_bytes(ctypes.byref(c))
 
 

@@ -650,6 +650,20 @@ def test_binding_refuses(sdm):
             f()
 
 
+def test_binding_refuses_sizes_beyond_its_fields(sdm):
+    """2^32 + 4 tokens or columns are not taken for 4."""
+    big, z = (1 << 32) + 4, torch.zeros(1, device="cuda")
+    x, w = z.expand(1, 1, big, 4), z.expand(1, 4, 4).contiguous()
+    u, A, Bm = z.expand(1, big, 4), z.expand(4, 16).contiguous(), z.expand(1, big, 1, 16)
+    r = z.expand(2, big)
+    for f in (lambda: sdm.short_conv(x, w), lambda: sdm.short_conv_backward(x, w, x),
+              lambda: sdm.selective_scan(u, u, A, Bm, Bm),
+              lambda: sdm.selective_scan_backward(u, u, A, Bm, Bm, u),
+              lambda: sdm.block_norm(r, r), lambda: sdm.block_norm_backward(r, r, r, None)):
+        with pytest.raises(ValueError, match="too large"):
+            f()
+
+
 def test_empty_calls(sdm):
     """No tokens: states stay (or start at zero when fresh), gradients pass through."""
     w, st = torch.ones(1, 8, 4, device="cuda"), torch.ones(2, 1, 3, 8, device="cuda")

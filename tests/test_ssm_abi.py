@@ -177,3 +177,17 @@ def test_norm_arguments(lib):
                                            p(P), p(P), dgate, None, dw, None, ws, n, None)
     assert bwd(dgate=p(P)) == 1 and bwd(dw=p(P)) == 1
     assert bwd(ws=None) == 7 and bwd(n=ctypes.c_size_t(need - 1)) == 7 and bwd(ws=p(P + 4)) == 4
+
+
+@pytest.mark.parametrize("dims,sizes", [
+    ("_conv_dims", (2, 4, 64, 128, 4, 1, 1, 0)), ("_scan_dims", (2, 64, 128, 16, 2, 1, 1, 0)),
+    ("_norm_dims", (10, 64, 0, 0, 1, 1e-6))])
+def test_binding_sizes(dims, sizes):
+    """The binding's dims structures hold what they are given or refuse it."""
+    import sparse_state_linear_score_b200 as m
+    f = getattr(m, dims)
+    f(*sizes)
+    for i, v in enumerate(sizes):
+        if isinstance(v, int) and not (dims == "_norm_dims" and i == 0):
+            with pytest.raises(ValueError, match="too large"):
+                f(*sizes[:i], (1 << 32) + v, *sizes[i + 1:])
