@@ -583,6 +583,66 @@ def test_streams_and_graphs(sdm):
     assert all(torch.equal(a, b2) for a, b2 in zip(outs[1], want))
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T", [1, 90])
+def test_layouts(sdm, T, dtype):
+    """Token-major and sequence-minor views, and inputs that are broadcast over sequences, heads or
+    tokens, give what contiguous copies give; gradients of broadcast inputs are of the whole view."""
+    g, dt, B, H, d, D, G, N = gen(5), DT[dtype], 3, 2, 8, 24, 2, 16
+    w = rnd(g, H, d, 4).cuda()
+    A = -(torch.rand(D, N, generator=g) + 0.1).cuda()
+
+    def same(f, views):
+        got, want = f(*views), f(*(v.contiguous() for v in views))
+        for a, b in zip(*((r if isinstance(r, tuple) else [r[k] for k in sorted(r)])
+                          for r in (got, want))):
+            assert torch.equal(a, b)
+
+    def conv(x, dy):
+        st = torch.ones(B, H, 3, d, dtype=dt, device="cuda")
+        return sdm.short_conv(x, w, state=st), st, *sdm.short_conv_backward(x, w, dy).values()
+
+    def scan(u, de, Bm, Cm, dy):
+        h = torch.ones(B, D, N, device="cuda")
+        y = sdm.selective_scan(u, de, A, Bm, Cm, z=u, state=h)
+        r = sdm.selective_scan_backward(u, de, A, Bm, Cm, dy, z=u)
+        return y, h, *(r[k] for k in sorted(r))
+
+    x = rnd(g, B, T, H, d, dt=dt).cuda().transpose(1, 2)
+    xs = rnd(g, H, T, B, d, dt=dt).cuda().permute(2, 0, 1, 3)
+    for views in ((x, xs), (xs, x), (x[:1].expand(B, H, T, d), xs[:, :1].expand(B, H, T, d)),
+                  (x[:, :, :1].expand(B, H, T, d), x)):
+        same(conv, views)
+    u = rnd(g, T, B, D, dt=dt).cuda().transpose(0, 1)
+    de = rnd(g, 1, T, D, dt=dt).cuda().expand(B, T, D)
+    Bm = rnd(g, B, G, T, N, dt=dt).cuda().transpose(1, 2)
+    Cm = rnd(g, 1, T, 1, N, dt=dt).cuda().expand(B, T, G, N)
+    same(scan, (u, de, Bm, Cm, de))
+    same(scan, (de, u, Cm, Bm, u[:, :1].expand(B, T, D)))
+
+
+def test_lengths_are_clamped(sdm):
+    """Lengths below zero and beyond the call are taken as 0 and T."""
+    B, T = 3, 20
+    raw, ln = (torch.tensor(v, dtype=torch.int32, device="cuda")
+               for v in ([-7, T + 5, 1 << 30], [0, T, T]))
+    c, o, st, dy, _ = scan_case(B, T, 12, 16, 1, "f32", True, True)
+    cg, og = put_scan(c, o, None, None)
+    x, w, b, cst, cdy, _, _ = conv_case(B, 2, T, 16, 4, "f32", "silu", True, None)
+    out = []
+    for v in (raw, ln):
+        h, s = st.cuda(), cst.cuda()
+        r = [sdm.selective_scan(*cg.values(), **og, state=h, lens=v), h,
+             sdm.short_conv(up(x), up(w), up(b), state=s, lens=v), s]
+        for q in (sdm.selective_scan_backward(*cg.values(), up(dy), **og, lens=v),
+                  sdm.short_conv_backward(up(x), up(w), up(cdy), up(b), lens=v)):
+            r += [q[k] for k in sorted(q)]
+        t = [a[:, :1].contiguous() for a in (cg["u"], cg["delta"], cg["B"], cg["C"])]
+        r.append(sdm.selective_scan(t[0], t[1], cg["A"], *t[2:], state=h, lens=v))
+        out.append(r + [h])
+    assert all(torch.equal(a, b2) for a, b2 in zip(*out))
+
+
 def test_long_offsets(sdm):
     """Offsets beyond 2^31 elements: two sequences far apart in one buffer, and a state behind
     them."""
