@@ -108,9 +108,20 @@ SDM_DEV void conv_load_window(const ConvArgs<T>& a, const T* x, const T* state, 
     }
 }
 
+// What a lane's loads pass through: a ring in shared memory that cp.async fills, three groups of four
+// tokens ahead (whole vectors; each lane reads what it has copied itself), or registers, one group
+// ahead.
+constexpr int CONV_GRP = 4, CONV_RING = 4;
+template <typename T, int V>
+__host__ __device__ constexpr size_t conv_ring_bytes(int streams) {
+    return V == 4 ? (size_t)CONV_WARPS * CONV_RING * CONV_GRP * streams * 32 * V * sizeof(T) : 0;
+}
+
 template <typename T, int V, int K>
 __global__ void __launch_bounds__(CONV_WARPS * 32) short_conv_kernel(ConvArgs<T> a) {
-    constexpr int U = 8, N = Pairs<V>::N;  // U tokens' loads are in flight together
+    constexpr bool RING = V == 4;
+    constexpr int U = RING ? CONV_GRP : 8, N = Pairs<V>::N;  // U tokens of a group
+    extern __shared__ __align__(16) char smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int nv = a.d / V;
     const long long cv = (long long)blockIdx.x * 32 + lane;
@@ -127,14 +138,24 @@ __global__ void __launch_bounds__(CONV_WARPS * 32) short_conv_kernel(ConvArgs<T>
     T* state = a.state ? a.state + ((long long)b * a.H + h) * (K - 1) * a.d + c : nullptr;
 
     Raw<T, V> in[U];
-    auto fetch = [&](int t) {
+    T* ring = reinterpret_cast<T*>(smem) + (warp * CONV_RING * U * 32 + lane) * V;
+    auto fetch = [&](int k, int t) {  // tokens t.. into group k of the ring, or into registers
+        if constexpr (RING) {
 #pragma unroll
-        for (int i = 0; i < U; ++i)
-            if (t + i < t1) in[i].load(x + (t + i) * a.x.st);
+            for (int i = 0; i < U; ++i)
+                async_copy<V * sizeof(T)>(ring + (k % CONV_RING * U + i) * 32 * V, x + (t + i) * a.x.st,
+                                          t + i < t1 ? V * (int)sizeof(T) : 0);
+            async_commit();
+        } else {
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                in[i].clear();
+                if (t + i < t1) in[i].load(x + (t + i) * a.x.st);
+            }
+        }
     };
 #pragma unroll
-    for (int i = 0; i < U; ++i) in[i].clear();
-    fetch(t0);
+    for (int k = 0; k < (RING ? CONV_RING - 1 : 1); ++k) fetch(k, t0 + k * U);
     f32x2 w[K][N], bias[N], win[K][N];
     conv_load_filter<V, K>(a.w, a.bias, (long long)h * a.d + c, w, bias);
     conv_load_window<T, V, K>(a, x, a.fresh ? nullptr : state, t0, len, win);
@@ -158,11 +179,17 @@ __global__ void __launch_bounds__(CONV_WARPS * 32) short_conv_kernel(ConvArgs<T>
 
     auto walk = [&](auto act) {
         constexpr bool ACT = decltype(act)::value;
-        for (int t = t0; t < t1; t += U) {
+        for (int t = t0, k = 0; t < t1; t += U, ++k) {
             f32x2 cur[U][N];
+            if constexpr (RING) {
+                async_wait<CONV_RING - 2>();
+#pragma unroll
+                for (int i = 0; i < U; ++i) in[i].load(ring + (k % CONV_RING * U + i) * 32 * V);
+            }
 #pragma unroll
             for (int i = 0; i < U; ++i) in[i].pairs(cur[i]);
-            fetch(t + U);
+            if constexpr (RING) fetch(k + CONV_RING - 1, t + (CONV_RING - 1) * U);
+            else fetch(k + 1, t + U);
 #pragma unroll
             for (int i = 0; i < U; ++i) {
                 f32x2 o[N];
@@ -182,15 +209,6 @@ __global__ void __launch_bounds__(CONV_WARPS * 32) short_conv_kernel(ConvArgs<T>
     };
     if (a.act) walk(Flag<true>());
     else walk(Flag<false>());
-}
-
-// What a lane's loads of the gradient pass through: a ring in shared memory that cp.async fills,
-// three groups of four tokens ahead (whole vectors; each lane reads what it has copied itself), or
-// registers, one group ahead.
-constexpr int CONV_GRP = 4, CONV_RING = 4;
-template <typename T, int V>
-__host__ __device__ constexpr size_t conv_ring_bytes() {
-    return V == 4 ? (size_t)CONV_WARPS * CONV_RING * CONV_GRP * 2 * 32 * V * sizeof(T) : 0;
 }
 
 // A warp takes every (gridDim.y * CONV_WARPS)-th run and sums its share of dw and dbias in

@@ -128,11 +128,11 @@ template <typename T, int V, int K>
 sdm_status launch_conv(const ConvArgs<T>& a, const ConvPlan& p, bool bwd, cudaStream_t s) {
     const dim3 grid(p.gx, p.gy);
     if (bwd) {
-        constexpr size_t ring = conv_ring_bytes<T, V>();
+        constexpr size_t ring = conv_ring_bytes<T, V>(2);
         if (!allow_smem(short_conv_bwd_kernel<T, V, K>, ring)) return SDM_ERR_CUDA;
         short_conv_bwd_kernel<T, V, K><<<grid, CONV_WARPS * 32, ring, s>>>(a);
     } else {
-        short_conv_kernel<T, V, K><<<grid, CONV_WARPS * 32, 0, s>>>(a);
+        short_conv_kernel<T, V, K><<<grid, CONV_WARPS * 32, conv_ring_bytes<T, V>(1), s>>>(a);
     }
     return launched();
 }
