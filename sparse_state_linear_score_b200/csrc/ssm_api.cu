@@ -97,13 +97,20 @@ struct ConvPlan {
     unsigned gx, gy;
 };
 
-// Tokens of a run: as long as there are enough warps (24 an SM hide the loads' latency), since a
-// run reads K-1 tokens of its neighbour.
-ConvPlan conv_plan(const sdm_conv_dims* d, int V) {
+// Tokens of a run: eight; twelve, what the ring holds at once, where that leaves 12 warps an SM; more,
+// since a run reads K-1 tokens of its neighbour, as long as there are 24 warps an SM, or 48 where the
+// sequences have lengths and runs behind them end at once.  (bf16, K = 4: 2 x 4 x 512 x 128 4.4 us
+// in runs of 8, 4.7 us of 12; 2 x 4 x 4096 x 128 8.4 us in runs of 8, 7.1 us of 12, 8.9 us of 32;
+// 8 x 16 x 2048 x 128 31 us in runs of 64, 34.7 and 33.5 us of 32 and 128; 8 x 16 x 8192 x 64 55 us in
+// runs of 128, 57 us of 64, half of it padding 40 and 35 us.)
+ConvPlan conv_plan(const sdm_conv_dims* d, int V, bool lens) {
     ConvPlan p;
     p.gx = (unsigned)ceil_div((long long)d->H * (d->d / V), 32);
-    p.run = CONV_RUN_MIN;
-    while (p.run < 256 && (long long)p.gx * d->B * ceil_div(d->T, 2 * p.run) >= kSms * 24) p.run *= 2;
+    auto warps = [&](int run) { return (long long)p.gx * d->B * ceil_div(d->T, run); };
+    p.run = V == 4 && warps(CONV_GRP * (CONV_RING - 1)) >= kSms * 12 ? CONV_GRP * (CONV_RING - 1)
+                                                                     : CONV_RUN_MIN;
+    for (int next = V == 4 ? 32 : 16; next <= 256 && warps(next) >= kSms * (lens ? 48 : 24); next *= 2)
+        p.run = next;
     while (ceil_div((long long)d->B * ceil_div(d->T, p.run), CONV_WARPS) > kMaxGrid) p.run *= 2;
     p.runs = (int)std::max(1LL, ceil_div(d->T, p.run));
     p.gy = (unsigned)ceil_div((long long)d->B * p.runs, CONV_WARPS);
@@ -170,7 +177,7 @@ sdm_status run_conv(const sdm_conv_dims* d, const sdm_view* x, const float* w, c
     ConvArgs<T> a = conv_args<T>(d, x, w, bias, state, lens);
     a.y = view<T>(y);
     const bool v4 = d->d % 4 == 0 && vec4_ok(x, d->x_dtype) && vec4_ok(y, d->x_dtype);
-    const ConvPlan p = conv_plan(d, v4 ? 4 : 1);
+    const ConvPlan p = conv_plan(d, v4 ? 4 : 1, lens != nullptr);
     a.run = p.run, a.runs = p.runs;
     return v4 ? launch_conv_k<T, 4>(a, p, false, s) : launch_conv_k<T, 1>(a, p, false, s);
 }
