@@ -530,54 +530,59 @@ NormArgs norm_args(const sdm_norm_dims* d, const void* r, const void* f, const f
 }
 
 struct NormPlan {
-    unsigned threads, blocks;  // blocks of a row: 1, 2 or 4
-    unsigned groups;           // rows in work at a time
+    unsigned threads, blocks;  // a row's block, blocks that take rows in turn
+    size_t smem;
 };
 
-// Eight values a thread, 4096 columns a block.  The forward pass keeps 1024 threads of blocks an SM
-// (16 blocks at most), the gradient 512, so that few shares of its sums are written.
+bool norm_wide(int D) { return D > NORM_COLS; }
+
+// Up to 4096 columns eight values a thread.  The forward pass keeps 1024 threads of blocks an SM (16
+// blocks at most), the gradient 512, so that few shares of its sums are written.  Wider rows: the
+// forward pass 256 threads and a row of floats in shared memory, the gradient three of them; 512
+// threads where only one block's fits an SM.
 NormPlan norm_plan(const sdm_norm_dims* d, bool bwd) {
-    NormPlan p;
-    const int cols = std::min(d->D, NORM_COLS);
-    p.threads = (unsigned)(ceil_div(ceil_div(cols, 8), 32) * 32);
-    p.blocks = d->D <= NORM_COLS ? 1 : (d->D <= 2 * NORM_COLS ? 2 : 4);
-    const long long per_sm = std::min<long long>(16, (bwd ? 512 : 1024) / p.threads);
-    p.groups = (unsigned)std::min<long long>(d->rows, std::max(1LL, kSms * per_sm / p.blocks));
+    NormPlan p{};
+    long long per_sm;
+    if (norm_wide(d->D)) {
+        p.smem = (size_t)ceil_div(d->D, 4) * 16 * (bwd ? 3 : 1);
+        per_sm = std::min<long long>(bwd ? 2 : 4, 220 * 1024 / (p.smem + 3 * 1024));
+        p.threads = bwd && per_sm < 2 ? NORM_THREADS : NORM_WIDE;
+    } else {
+        p.threads = (unsigned)(ceil_div(ceil_div(d->D, 8), 32) * 32);
+        per_sm = std::min<long long>(16, (bwd ? 512 : 1024) / p.threads);
+    }
+    p.blocks = (unsigned)std::min<long long>(d->rows, kSms * per_sm);
     return p;
 }
 
-template <bool VEC, bool CL, int DT, bool ALL>
+template <bool VEC, int DT>
+sdm_status launch_norm_wide(const NormArgs& a, bool bwd, const NormPlan& p, cudaStream_t s) {
+    auto kernel = bwd ? block_norm_bwd_wide_kernel<VEC, DT> : block_norm_wide_kernel<VEC, DT>;
+    if (!allow_smem(kernel, p.smem)) return SDM_ERR_CUDA;
+    kernel<<<p.blocks, p.threads, p.smem, s>>>(a);
+    return launched();
+}
+
+template <bool VEC, int DT, bool ALL>
 sdm_status launch_norm(const NormArgs& a, bool bwd, const NormPlan& p, cudaStream_t s) {
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = p.blocks, attr.val.clusterDim.y = 1, attr.val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(p.groups * p.blocks);
-    cfg.blockDim = dim3(p.threads);
-    cfg.stream = s;
-    cfg.attrs = &attr;
-    cfg.numAttrs = CL ? 1 : 0;
-    const cudaError_t e = bwd ? cudaLaunchKernelEx(&cfg, block_norm_bwd_kernel<VEC, CL, DT, ALL>, a)
-                              : cudaLaunchKernelEx(&cfg, block_norm_kernel<VEC, CL, DT, ALL>, a);
-    (void)cudaGetLastError();
-    return e == cudaSuccess ? SDM_OK : SDM_ERR_CUDA;
+    if (bwd) block_norm_bwd_kernel<VEC, DT, ALL><<<p.blocks, p.threads, 0, s>>>(a);
+    else block_norm_kernel<VEC, DT, ALL><<<p.blocks, p.threads, 0, s>>>(a);
+    return launched();
 }
 
 template <int DT>
 sdm_status launch_norm_typed(const NormArgs& a, bool bwd, const NormPlan& p, cudaStream_t s) {
     const bool all = a.gate && a.w_post && a.scale && a.w_pre &&
                      (bwd ? a.dr_out && a.dn && a.dr && a.df && a.dgate : a.r_out && a.n);
-    return all ? launch_norm<true, false, DT, true>(a, bwd, p, s)
-               : launch_norm<true, false, DT, false>(a, bwd, p, s);
+    return all ? launch_norm<true, DT, true>(a, bwd, p, s) : launch_norm<true, DT, false>(a, bwd, p, s);
 }
 
 // Whole pieces in one block are compiled for their types; wider rows and odd widths look the types
 // up.
 sdm_status launch_norm_any(const NormArgs& a, bool bwd, const NormPlan& p, cudaStream_t s) {
-    if (a.D % 4 != 0)
-        return p.blocks > 1 ? launch_norm<false, true, -1, false>(a, bwd, p, s)
-                            : launch_norm<false, false, -1, false>(a, bwd, p, s);
-    if (p.blocks > 1) return launch_norm<true, true, -1, false>(a, bwd, p, s);
+    if (norm_wide(a.D))
+        return a.D % 4 ? launch_norm_wide<false, -1>(a, bwd, p, s) : launch_norm_wide<true, -1>(a, bwd, p, s);
+    if (a.D % 4) return launch_norm<false, -1, false>(a, bwd, p, s);
     switch (a.rb | a.fb << 1 | a.xb << 2) {
         case 0: return launch_norm_typed<0>(a, bwd, p, s);
         case 1: return launch_norm_typed<1>(a, bwd, p, s);
@@ -724,7 +729,7 @@ sdm_status sdm_block_norm(const sdm_norm_dims* dims, const void* r, const void* 
 
 size_t sdm_block_norm_backward_workspace_bytes(const sdm_norm_dims* dims) {
     if (check_norm(dims) != SDM_OK) return 0;
-    return up256(std::max<size_t>(1, norm_plan(dims, true).groups) * 3 * dims->D * 4);
+    return up256(std::max<size_t>(1, norm_plan(dims, true).blocks) * 3 * dims->D * 4);
 }
 
 sdm_status sdm_block_norm_backward(const sdm_norm_dims* dims, const void* r, const void* f,
@@ -749,7 +754,7 @@ sdm_status sdm_block_norm_backward(const sdm_norm_dims* dims, const void* r, con
     const NormPlan p = norm_plan(dims, true);
     if (dims->rows > 0 && (e = launch_norm_any(a, true, p, stream))) return e;
     norm_sum_kernel<<<(unsigned)ceil_div(3LL * dims->D, 32), 32 * SUM_SEG, 0, stream>>>(
-        a.part, (int)p.groups, dims->D, dscale, dw_post, dw_pre);
+        a.part, (int)p.blocks, dims->D, dscale, dw_post, dw_pre);
     return launched();
 }
 
