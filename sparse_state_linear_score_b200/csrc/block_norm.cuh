@@ -256,13 +256,13 @@ __global__ void __launch_bounds__(NORM_THREADS, 2) block_norm_kernel(NormArgs a)
 // same ones in every pass, with the row as floats in shared memory between them: f and the sum of
 // its squares; o, which replaces f, r_out and the sum of o's squares; n.
 constexpr int NORM_U = 4;  // pieces whose loads are in flight together
-template <bool VEC, int DT>
+template <bool VEC>
 __global__ void __launch_bounds__(NORM_WIDE, 4) block_norm_wide_kernel(NormArgs a) {
     constexpr int U = NORM_U, H = NORM_U / 2;
     extern __shared__ __align__(16) char smem[];
     __shared__ __align__(16) NormSums s_sum;
     ulonglong2* kept = reinterpret_cast<ulonglong2*>(smem);  // a piece each
-    const bool rb = DT < 0 ? a.rb : DT & 1, fb = DT < 0 ? a.fb : DT & 2, xb = DT < 0 ? a.xb : DT & 4;
+    const bool rb = a.rb, fb = a.fb, xb = a.xb;
     const bool has_gate = a.gate, has_post = a.w_post, has_scale = a.scale;
     RowSum red{s_sum, 0};
     s_sum.clear();
@@ -347,11 +347,11 @@ __global__ void __launch_bounds__(NORM_WIDE, 4) block_norm_wide_kernel(NormArgs 
     }
 }
 
-template <bool VEC, int DT, bool ALL>
+template <int DT, bool ALL>
 __global__ void __launch_bounds__(NORM_THREADS, 1) block_norm_bwd_kernel(NormArgs a) {
     constexpr int P = NORM_P, N = 2;
     __shared__ __align__(16) NormSums s_sum;
-    const bool rb = DT < 0 ? a.rb : DT & 1, fb = DT < 0 ? a.fb : DT & 2, xb = DT < 0 ? a.xb : DT & 4;
+    const bool rb = DT & 1, fb = DT & 2, xb = DT & 4;
     const bool has_gate = ALL || a.gate, has_post = ALL || a.w_post, has_scale = ALL || a.scale,
                has_pre = ALL || a.w_pre, has_dn = ALL || a.dn, has_dr = ALL || a.dr_out,
                out_dr = ALL || a.dr, out_df = ALL || a.df, out_dg = ALL || a.dgate;
@@ -365,12 +365,12 @@ __global__ void __launch_bounds__(NORM_THREADS, 1) block_norm_bwd_kernel(NormArg
 #pragma unroll
         for (int v = 0; v < N; ++v) aw[i][v] = as[i][v] = aq[i][v] = zero;
     const float inv_d = 1.f / (float)a.D;
-    NormRaw<VEC> rf[P], rr[P], rg[P], rn[P], rd[P];
+    NormRaw<true> rf[P], rr[P], rg[P], rn[P], rd[P];
     auto fetch = [&](long long row) {
         const long long base = row * a.D;
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-            const int c = (i * blockDim.x + threadIdx.x) * NORM_V, cnt = min(NORM_V, a.D - c);
+            const int c = (i * blockDim.x + threadIdx.x) * NORM_V, cnt = NORM_V;
             rf[i].clear();
             rr[i].clear();
             rg[i].clear();
@@ -419,12 +419,12 @@ __global__ void __launch_bounds__(NORM_THREADS, 1) block_norm_bwd_kernel(NormArg
         // f becomes f^ (f itself without the norm), g the gate's sigmoid
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-            const int c = (i * blockDim.x + threadIdx.x) * NORM_V, cnt = min(NORM_V, a.D - c);
+            const int c = (i * blockDim.x + threadIdx.x) * NORM_V, cnt = NORM_V;
             if (c >= a.D) continue;
             f32x2 wp[N], sc[N], wq[N];
-            norm_weight<VEC>(has_post, a.w_post, c, cnt, wp);
-            norm_weight<VEC>(has_scale, a.scale, c, cnt, sc);
-            norm_weight<VEC>(has_pre, a.w_pre, c, cnt, wq);
+            norm_weight<true>(has_post, a.w_post, c, cnt, wp);
+            norm_weight<true>(has_scale, a.scale, c, cnt, sc);
+            norm_weight<true>(has_pre, a.w_pre, c, cnt, wq);
 #pragma unroll
             for (int v = 0; v < N; ++v) {
                 f[i][v] = mul2(f[i][v], rf1);
@@ -454,12 +454,12 @@ __global__ void __launch_bounds__(NORM_THREADS, 1) block_norm_bwd_kernel(NormArg
         }
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-            const int c = (i * blockDim.x + threadIdx.x) * NORM_V, cnt = min(NORM_V, a.D - c);
+            const int c = (i * blockDim.x + threadIdx.x) * NORM_V, cnt = NORM_V;
             if (c >= a.D) continue;
             f32x2 wp[N], sc[N], wq[N], dg[N];
-            norm_weight<VEC>(has_post, a.w_post, c, cnt, wp);
-            norm_weight<VEC>(has_scale, a.scale, c, cnt, sc);
-            norm_weight<VEC>(has_pre, a.w_pre, c, cnt, wq);
+            norm_weight<true>(has_post, a.w_post, c, cnt, wp);
+            norm_weight<true>(has_scale, a.scale, c, cnt, sc);
+            norm_weight<true>(has_pre, a.w_pre, c, cnt, wq);
 #pragma unroll
             for (int v = 0; v < N; ++v) {
                 const f32x2 oh = mul2(o[i][v], ro);
@@ -474,33 +474,34 @@ __global__ void __launch_bounds__(NORM_THREADS, 1) block_norm_bwd_kernel(NormArg
                 aw[i][v] = fma2(dp, f[i][v], aw[i][v]);
                 o[i][v] = mul2(rf1, fma2(f[i][v], mf, mul2(dp, wp[v])));
             }
-            if (out_dr) norm_store<VEC>(a.dr, rb, base + c, cnt, dr[i]);
-            if (out_dg) norm_store<VEC>(a.dgate, xb, base + c, cnt, dg);
-            if (out_df) norm_store<VEC>(a.df, fb, base + c, cnt, o[i]);
+            if (out_dr) norm_store<true>(a.dr, rb, base + c, cnt, dr[i]);
+            if (out_dg) norm_store<true>(a.dgate, xb, base + c, cnt, dg);
+            if (out_df) norm_store<true>(a.df, fb, base + c, cnt, o[i]);
         }
     }
     float* part = a.part + (long long)blockIdx.x * 3 * a.D;
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-        const int c = (i * blockDim.x + threadIdx.x) * NORM_V, cnt = min(NORM_V, a.D - c);
+        const int c = (i * blockDim.x + threadIdx.x) * NORM_V, cnt = NORM_V;
         if (c < a.D) {
-            norm_store<VEC>(part, false, c, cnt, as[i]);
-            norm_store<VEC>(part, false, (long long)a.D + c, cnt, aw[i]);
-            norm_store<VEC>(part, false, 2LL * a.D + c, cnt, aq[i]);
+            norm_store<true>(part, false, c, cnt, as[i]);
+            norm_store<true>(part, false, (long long)a.D + c, cnt, aw[i]);
+            norm_store<true>(part, false, 2LL * a.D + c, cnt, aq[i]);
         }
     }
 }
 
-// The gradient of rows of more than 4096 columns: two passes over a row's columns, the second of
-// which finds the inputs in L2; the columns' sums are kept in shared memory, each by its thread.
-template <bool VEC, int DT>
+// The gradient of rows of more than 4096 columns, and of odd widths, whose pieces' addresses and bounds
+// do not fit the registers beside a row: two passes over a row's columns, the second of which finds
+// the inputs in L2; the columns' sums are kept in shared memory, each by its thread.
+template <bool VEC>
 __global__ void __launch_bounds__(NORM_THREADS, 1) block_norm_bwd_wide_kernel(NormArgs a) {
     constexpr int U = 2;
     extern __shared__ __align__(16) char smem[];
     __shared__ __align__(16) NormSums s_sum;
     const int pieces = (a.D + NORM_V - 1) / NORM_V;
     ulonglong2* acc = reinterpret_cast<ulonglong2*>(smem);  // [3][pieces]: dscale, dw_post, dw_pre
-    const bool rb = DT < 0 ? a.rb : DT & 1, fb = DT < 0 ? a.fb : DT & 2, xb = DT < 0 ? a.xb : DT & 4;
+    const bool rb = a.rb, fb = a.fb, xb = a.xb;
     const bool has_gate = a.gate, has_post = a.w_post, has_scale = a.scale, has_pre = a.w_pre;
     RowSum red{s_sum, 0};
     s_sum.clear();

@@ -534,39 +534,31 @@ struct NormPlan {
     size_t smem;
 };
 
-bool norm_wide(int D) { return D > NORM_COLS; }
+bool norm_in_passes(int D, bool bwd) { return D > NORM_COLS || (bwd && D % 4 != 0); }
 
-// Up to 4096 columns eight values a thread.  The forward pass keeps 1024 threads of blocks an SM (16
-// blocks at most), the gradient 512, so that few shares of its sums are written.  Wider rows: the
-// forward pass 256 threads and a row of floats in shared memory, the gradient three of them; 512
-// threads where only one block's fits an SM.
+// Eight values a thread.  The forward pass keeps 1024 threads of blocks an SM (16 blocks at most), the
+// gradient 512, so that few shares of its sums are written.  In passes: up to 256 threads, and a row
+// of floats in shared memory, the gradient three of them; 512 threads where only one block's fit an SM.
 NormPlan norm_plan(const sdm_norm_dims* d, bool bwd) {
     NormPlan p{};
-    long long per_sm;
-    if (norm_wide(d->D)) {
+    const bool passes = norm_in_passes(d->D, bwd);
+    const int most = passes ? NORM_WIDE : NORM_THREADS;
+    p.threads = (unsigned)std::min<long long>(most, ceil_div(ceil_div(d->D, 8), 32) * 32);
+    long long per_sm = std::min<long long>(16, (bwd ? 512 : 1024) / p.threads);
+    if (passes) {
         p.smem = (size_t)ceil_div(d->D, 4) * 16 * (bwd ? 3 : 1);
-        per_sm = std::min<long long>(bwd ? 2 : 4, 220 * 1024 / (p.smem + 3 * 1024));
-        p.threads = bwd && per_sm < 2 ? NORM_THREADS : NORM_WIDE;
-    } else {
-        p.threads = (unsigned)(ceil_div(ceil_div(d->D, 8), 32) * 32);
-        per_sm = std::min<long long>(16, (bwd ? 512 : 1024) / p.threads);
+        per_sm = std::min<long long>(per_sm, 220 * 1024 / (p.smem + 3 * 1024));
+        if (bwd && per_sm == 1) p.threads = NORM_THREADS;
     }
     p.blocks = (unsigned)std::min<long long>(d->rows, kSms * per_sm);
     return p;
 }
 
-template <bool VEC, int DT>
+template <bool VEC>
 sdm_status launch_norm_wide(const NormArgs& a, bool bwd, const NormPlan& p, cudaStream_t s) {
-    auto kernel = bwd ? block_norm_bwd_wide_kernel<VEC, DT> : block_norm_wide_kernel<VEC, DT>;
+    auto kernel = bwd ? block_norm_bwd_wide_kernel<VEC> : block_norm_wide_kernel<VEC>;
     if (!allow_smem(kernel, p.smem)) return SDM_ERR_CUDA;
     kernel<<<p.blocks, p.threads, p.smem, s>>>(a);
-    return launched();
-}
-
-template <bool VEC, int DT, bool ALL>
-sdm_status launch_norm(const NormArgs& a, bool bwd, const NormPlan& p, cudaStream_t s) {
-    if (bwd) block_norm_bwd_kernel<VEC, DT, ALL><<<p.blocks, p.threads, 0, s>>>(a);
-    else block_norm_kernel<VEC, DT, ALL><<<p.blocks, p.threads, 0, s>>>(a);
     return launched();
 }
 
@@ -574,15 +566,21 @@ template <int DT>
 sdm_status launch_norm_typed(const NormArgs& a, bool bwd, const NormPlan& p, cudaStream_t s) {
     const bool all = a.gate && a.w_post && a.scale && a.w_pre &&
                      (bwd ? a.dr_out && a.dn && a.dr && a.df && a.dgate : a.r_out && a.n);
-    return all ? launch_norm<true, DT, true>(a, bwd, p, s) : launch_norm<true, DT, false>(a, bwd, p, s);
+    auto kernel = bwd ? (all ? block_norm_bwd_kernel<DT, true> : block_norm_bwd_kernel<DT, false>)
+                      : (all ? block_norm_kernel<true, DT, true> : block_norm_kernel<true, DT, false>);
+    kernel<<<p.blocks, p.threads, 0, s>>>(a);
+    return launched();
 }
 
-// Whole pieces in one block are compiled for their types; wider rows and odd widths look the types
-// up.
+// Rows of whole pieces that fit a block's registers are compiled for their types; the others look the
+// types up.
 sdm_status launch_norm_any(const NormArgs& a, bool bwd, const NormPlan& p, cudaStream_t s) {
-    if (norm_wide(a.D))
-        return a.D % 4 ? launch_norm_wide<false, -1>(a, bwd, p, s) : launch_norm_wide<true, -1>(a, bwd, p, s);
-    if (a.D % 4) return launch_norm<false, -1, false>(a, bwd, p, s);
+    if (norm_in_passes(a.D, bwd))
+        return a.D % 4 ? launch_norm_wide<false>(a, bwd, p, s) : launch_norm_wide<true>(a, bwd, p, s);
+    if (a.D % 4) {
+        block_norm_kernel<false, -1, false><<<p.blocks, p.threads, 0, s>>>(a);
+        return launched();
+    }
     switch (a.rb | a.fb << 1 | a.xb << 2) {
         case 0: return launch_norm_typed<0>(a, bwd, p, s);
         case 1: return launch_norm_typed<1>(a, bwd, p, s);
