@@ -16,7 +16,7 @@
 // one) the next row's loads issued ahead.
 // Measured: 8192 rows of 4096, r and f fp32, gate and n bf16, 95 us, 5.3 TB/s; gradient of 4099 rows,
 // all bf16, 72 us, 3.6 TB/s (a row's latency at one block an SM); 3395 rows of 8192, bf16, 69 us, 4.0
-// TB/s, gradient 192 us, 2.3 TB/s.
+// TB/s, gradient 192 us, 2.3 TB/s; odd widths, 4096 rows of 4095, 69 and 165 us.
 #pragma once
 
 #include "ssm_util.cuh"

@@ -19,9 +19,9 @@
 // of its steps.  The same walk computes those first (the exponentials once more),
 // scan_carry_kernel chains them, and every chunk's outputs start from its true state.
 //
-// Measured, 16 states: 2 sequences of 4096 tokens, 4096 channels, bf16, 271 us (119 us of
+// Measured, 16 states: 2 sequences of 4096 tokens, 4096 channels, bf16, 274 us (119 us of
 // exponentials; issue 60 %, exponential unit 54 %, shared memory 57 %, 1.7 warps a sub-partition);
-// one of 16384 tokens, 512 channels, fp32, 113 us in 37 chunks.
+// one of 16384 tokens, 512 channels, fp32, 114 us in 37 chunks.
 #pragma once
 
 #include "ssm_util.cuh"

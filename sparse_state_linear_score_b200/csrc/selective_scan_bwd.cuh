@@ -20,7 +20,7 @@
 //
 // Bound by issue and shared memory: about 155 instructions and 37 shared-memory cycles a token and
 // eight channels of 16 states.  2 sequences of 2048 tokens, 2048 channels, bf16: 266 us (issue 58 %,
-// shared memory 53 %), with the walks, carries and sums 359 us; three passes over the exponentials
+// shared memory 53 %), with the walks, carries and sums 361 us; three passes over the exponentials
 // alone are 90 us.
 #pragma once
 

@@ -9,9 +9,11 @@
 // of the flattened (head, channel) axis, whose filters stay in registers, and the last K-1 tokens
 // move through a register window, so each input is read from memory once (plus K-1 tokens where
 // runs meet, which L2 holds).  Loads are issued as they are stored and converted only when used: a
-// conversion behind a load waits for it (the gradient took 506 us so, 206 us without).
-// Measured, bf16, K = 4, caches cold: forward 2 x 4 x 4096 x 128 9.7 us; gradient 8 x 16 x 8192 x 64
-// 88 us, 4.3 TB/s, 55 % of the issue slots.
+// conversion behind a load waits for it (the gradient took 506 us so, 206 us without); through a
+// ring in shared memory they take no registers meanwhile (forward, 8 x 16 x 2048 x 128: 34.7 us with
+// eight tokens in registers, 31.6 us; eight taps 61 and 42 us).
+// Measured, bf16, K = 4, inputs not in L2: forward 2 x 4 x 4096 x 128 7.1 us, 8 x 16 x 2048 x 128 31 us,
+// 4.3 TB/s; gradient 8 x 16 x 8192 x 64 88 us, 4.3 TB/s, 55 % of the issue slots.
 #pragma once
 
 #include "ssm_util.cuh"

@@ -357,6 +357,10 @@ NORM = [  # rows, D, r, f, x, (w_post, gate, scale, w_pre)
     (700, 12, "bf16", "bf16", "f32", (1, 0, 0, 1)),
     (400, 6001, "bf16", "f32", "bf16", (1, 1, 1, 1)),
     (200, 12000, "f32", "bf16", "f32", (1, 1, 1, 1)),
+    # more wide rows than blocks
+    (700, 4104, "bf16", "f32", "bf16", (1, 1, 1, 1)),
+    (650, 4099, "f32", "f32", "f32", (0, 1, 1, 0)),
+    (601, 5001, "f32", "bf16", "f32", (1, 1, 1, 1)),
 ]
 
 
