@@ -338,6 +338,10 @@ __global__ void __launch_bounds__(CONV_WARPS * 32, K <= 4 ? 3 : 1) short_conv_bw
                 }
                 const int s = t + i - (K - 1);
                 if (t + i >= tend || (s < t0 && run > 0)) continue;  // the run before has it
+                if (s >= len) {  // zero, also where a filter is not finite
+#pragma unroll
+                    for (int p = 0; p < N; ++p) out[i][p] = dup2(0.f);
+                }
                 const int kept = s - len + K - 1;  // its row in the state after the call
                 if (a.dstate_end && kept >= 0 && kept < K - 1) {
                     f32x2 e[N];
@@ -355,7 +359,10 @@ __global__ void __launch_bounds__(CONV_WARPS * 32, K <= 4 ? 3 : 1) short_conv_bw
         } else {
             fetch(0, t0);
         }
-        conv_load_window<T, V, K>(a, x, state, t0, len, win);
+        // a run behind the sequence multiplies its window by zeros only: zero too, so that what lies
+        // before it (of an empty sequence, its state) reaches dw of no other sequence, finite or not
+        const bool behind = t0 >= len;
+        conv_load_window<T, V, K>(a, x, behind ? nullptr : state, t0, behind ? 0 : len, win);
 #pragma unroll
         for (int j = 0; j < K; ++j)
 #pragma unroll

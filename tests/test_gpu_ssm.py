@@ -140,6 +140,29 @@ def test_conv_calls_chain(sdm, cuts):
     assert torch.equal(torch.cat(parts, dim=2), whole) and torch.equal(s1, s2)
 
 
+@pytest.mark.parametrize("K,d,dtype", [(2, 7, "f32"), (4, 8, "bf16"), (4, 8, "f32"), (8, 12, "bf16")])
+def test_conv_backward_of_sequences_without_tokens(sdm, K, d, dtype):
+    """What an empty sequence's state holds, and the gradient that comes to it, are its own: the
+    filters' gradients are those of the others.  Behind a sequence dx is zero whatever the filters."""
+    B, H, T, lens = 3, 2, 40, [5, 0, 33]
+    x, w, b, st, dy, de, act = conv_case(B, H, T, d, K, dtype, "silu", True, lens)
+    ln = torch.tensor(lens, dtype=torch.int32).cuda()
+    xg, dyg = poison(x, lens, 2).cuda(), poison(dy, lens, 2).cuda()
+    st[1], de[1] = 0, 0
+    want = sdm.short_conv_backward(xg, up(w), dyg, up(b), state=up(st), lens=ln, dstate_end=up(de))
+    for bad in (float("nan"), float("inf")):
+        st[1], de[1] = bad, bad
+        g = sdm.short_conv_backward(xg, up(w), dyg, up(b), state=up(st), lens=ln, dstate_end=up(de))
+        for k in ("dx", "dw", "dbias"):
+            assert torch.equal(g[k], want[k]), (k, bad)
+        assert torch.equal(g["dstate"][::2], want["dstate"][::2])
+        assert torch.equal(g["dstate"][1].cpu().nan_to_num(7, 8), de[1].nan_to_num(7, 8))
+    w[0, 1], w[1, 3, 0] = float("nan"), float("inf")
+    g = sdm.short_conv_backward(xg, up(w), dyg, up(b), lens=ln)
+    for q, n in enumerate(lens):
+        assert (g["dx"][q, :, n:] == 0).all()
+
+
 # ---- selective scan ------------------------------------------------------------------------
 
 SCAN = [  # B, T, D, N, G, dtype, softplus, opt (z, D, dt_bias), lens, view
