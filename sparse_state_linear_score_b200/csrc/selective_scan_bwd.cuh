@@ -14,6 +14,10 @@
 // lane, so that a group's 8 x 4 states and decays fit.  The next tile's rows are on their way
 // (cp.async) meanwhile.
 //
+// Tokens behind the sequence have a step and inputs of zero, which leave the sums as they are only
+// while the states and what comes to them are finite (an empty sequence's need not be), so their
+// outputs, and dA of a chunk without tokens, are written as zero.
+//
 // dB and dC sum over channels: over a warp's channels by shuffles that halve the number of values
 // with each step, over its tiles and then the block's warps in shared memory, over blocks by
 // scan_bc_sum_kernel, all in a fixed order.
@@ -362,7 +366,7 @@ __global__ void __launch_bounds__(BWD_WARPS * 32, 3) scan_bwd_kernel(ScanBwdArgs
             dD = fma2(g2, u2, dD);
             dbias = add2(dbias, vdd);
             if (t < tend) {
-                put(du + t * A.du.st, vdu);
+                put(du + t * A.du.st, vdu & inside(e));
                 put(dd + t * A.ddelta.st, vdd);
                 if (gate) {
                     Vec<2>::load(w.z[p] + e, z);
@@ -398,7 +402,7 @@ __global__ void __launch_bounds__(BWD_WARPS * 32, 3) scan_bwd_kernel(ScanBwdArgs
             for (int i = 0; i < NPT; ++i)
                 if (n0 + i < a.N) {
                     const long long cn = (long long)c * a.N + n0 + i;
-                    A.part_a[pc * a.D * a.N + cn] = dv[i];
+                    A.part_a[pc * a.D * a.N + cn] = t1 > t0 ? dv[i] : 0.f;
                     if (chunk == 0 && A.dstate) A.dstate[(long long)b * a.D * a.N + cn] = gv[i];
                 }
         }
@@ -412,7 +416,8 @@ __global__ void __launch_bounds__(BWD_WARPS * 32, 3) scan_bwd_kernel(ScanBwdArgs
             float sum = 0.f;
 #pragma unroll
             for (int q = 0; q < BWD_WARPS; ++q) sum += sh.w[q].acc[e];
-            A.part_bc[(((((long long)blk * a.B + b) * a.T_ + t) * a.G + g) * 2 + k / NN) * a.N + n] = sum;
+            A.part_bc[(((((long long)blk * a.B + b) * a.T_ + t) * a.G + g) * 2 + k / NN) * a.N + n] =
+                t < t1 ? sum : 0.f;
         }
     }
 }

@@ -363,6 +363,38 @@ def test_scan_outputs_are_reproducible(sdm):
     assert all(torch.equal(a, b) for a, b in zip(*runs))
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,N", [(20, 16), (90, 16), (90, 5)])
+def test_scan_backward_of_sequences_without_tokens(sdm, T, N, dtype):
+    """What an empty sequence's state holds, and the gradient that comes to it, are its own: the
+    sums over the batch are those of the others.  Behind a sequence every gradient is zero, whatever
+    comes to the state at its end."""
+    B, D, G, lens = 3, 12, 2, [T, 0, 5]
+    c, o, st, dy, de = scan_case(B, T, D, N, G, dtype, True, True)
+    ln = torch.tensor(lens, dtype=torch.int32).cuda()
+    cg, og = put_scan(c, o, lens, None)
+    dyg = poison(dy, lens, 1).cuda()
+
+    def run(**kw):
+        return sdm.selective_scan_backward(*cg.values(), dyg, **{**og, **kw}, state=up(st), lens=ln,
+                                           dstate_end=up(de))
+    st[1], de[1] = 0, 0
+    want = run()
+    for bad in (float("nan"), float("inf")):
+        st[1], de[1] = bad, bad
+        g = run()
+        for k in g:
+            if k != "dstate":
+                assert torch.equal(g[k], want[k]), (k, bad)
+        assert torch.equal(g["dstate"][::2], want["dstate"][::2])
+        assert torch.equal(g["dstate"][1].cpu().nan_to_num(7, 8), de[1].nan_to_num(7, 8))
+    de[2] = float("inf")
+    g = run(D=torch.full((D,), float("inf"), device="cuda"))
+    for k in ("du", "ddelta", "dz", "dB", "dC"):
+        for q, n in enumerate(lens):
+            assert (g[k][q, n:] == 0).all(), k
+
+
 # ---- block norms ---------------------------------------------------------------------------
 
 NORM = [  # rows, D, r, f, x, (w_post, gate, scale, w_pre)
