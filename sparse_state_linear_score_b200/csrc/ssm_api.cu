@@ -72,11 +72,12 @@ bool vec4_ok(const sdm_view* v, int32_t dtype) {
 }
 
 // Dynamic shared memory beyond what a kernel gets unasked: 48 KB, of which these kernels' own arrays
-// take 20 KB at most.
+// take 20 KB at most.  `most` is what any call of the kernel takes: the limit is the kernel's, and
+// another host thread that set it to less would make this call's launch fail.
 template <typename K>
-bool allow_smem(K kernel, size_t bytes) {
+bool allow_smem(K kernel, size_t bytes, size_t most) {
     if (bytes <= 28 * 1024) return true;
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) ==
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most) ==
            cudaSuccess;
 }
 
@@ -136,7 +137,7 @@ sdm_status launch_conv(const ConvArgs<T>& a, const ConvPlan& p, bool bwd, cudaSt
     const dim3 grid(p.gx, p.gy);
     if (bwd) {
         constexpr size_t ring = conv_ring_bytes<T, V>(2);
-        if (!allow_smem(short_conv_bwd_kernel<T, V, K>, ring)) return SDM_ERR_CUDA;
+        if (!allow_smem(short_conv_bwd_kernel<T, V, K>, ring, ring)) return SDM_ERR_CUDA;
         short_conv_bwd_kernel<T, V, K><<<grid, CONV_WARPS * 32, ring, s>>>(a);
     } else {
         short_conv_kernel<T, V, K><<<grid, CONV_WARPS * 32, conv_ring_bytes<T, V>(1), s>>>(a);
@@ -319,7 +320,7 @@ template <typename T, int NPT, int LN, int MODE, bool ODD>
 sdm_status launch_walk_t(const ScanArgs<T>& a, int runs, cudaStream_t s) {
     constexpr int WCH = 32 / LN;
     constexpr size_t smem = sizeof(ScanShared<T, NPT, LN, MODE>);
-    if (!allow_smem(scan_walk_kernel<T, NPT, LN, MODE, ODD>, smem)) return SDM_ERR_CUDA;
+    if (!allow_smem(scan_walk_kernel<T, NPT, LN, MODE, ODD>, smem, smem)) return SDM_ERR_CUDA;
     const unsigned gx = (unsigned)(a.G * ceil_div(a.D / a.G, WCH));
     scan_walk_kernel<T, NPT, LN, MODE, ODD><<<dim3(gx, runs, a.B), 32, smem, s>>>(a);
     return launched();
@@ -449,7 +450,7 @@ sdm_status launch_scan_bwd_t(const ScanBwdArgs<T>& A, const ScanBwdPlan& p,
     ScanBwdArgs<T> B = A;
     set_pieces(B.s, v, 32 / LN, NN);
     constexpr size_t smem = sizeof(BwdShared<T, LN>);
-    if (!allow_smem(scan_bwd_kernel<T, LN>, smem)) return SDM_ERR_CUDA;
+    if (!allow_smem(scan_bwd_kernel<T, LN>, smem, smem)) return SDM_ERR_CUDA;
     scan_bwd_kernel<T, LN>
         <<<dim3((unsigned)(a.G * p.blocks), p.nchunk, a.B), BWD_WARPS * 32, smem, s>>>(B);
     return launched();
@@ -511,10 +512,12 @@ sdm_status check_scan_in(const sdm_scan_dims* d, const sdm_view* u, const sdm_vi
 
 // ---- block norms ---------------------------------------------------------------------------
 
+constexpr int kNormMaxD = 16384;
+
 sdm_status check_norm(const sdm_norm_dims* d) {
     if (!d) return SDM_ERR_ARG;
     if (!known(d->r_dtype) || !known(d->f_dtype) || !known(d->x_dtype)) return SDM_ERR_DTYPE;
-    if (d->rows < 0 || d->D < 1 || d->D > 16384) return SDM_ERR_SHAPE;
+    if (d->rows < 0 || d->D < 1 || d->D > kNormMaxD) return SDM_ERR_SHAPE;
     if (!(d->eps >= 0.f)) return SDM_ERR_ARG;
     return SDM_OK;
 }
@@ -534,6 +537,8 @@ struct NormPlan {
     size_t smem;
 };
 
+size_t norm_smem(int D, bool bwd) { return (size_t)ceil_div(D, 4) * 16 * (bwd ? 3 : 1); }  // in passes
+
 bool norm_in_passes(int D, bool bwd) { return D > NORM_COLS || (bwd && D % 4 != 0); }
 
 // Eight values a thread.  The forward pass keeps 1024 threads of blocks an SM (16 blocks at most), the
@@ -546,7 +551,7 @@ NormPlan norm_plan(const sdm_norm_dims* d, bool bwd) {
     p.threads = (unsigned)std::min<long long>(most, ceil_div(ceil_div(d->D, 8), 32) * 32);
     long long per_sm = std::min<long long>(16, (bwd ? 512 : 1024) / p.threads);
     if (passes) {
-        p.smem = (size_t)ceil_div(d->D, 4) * 16 * (bwd ? 3 : 1);
+        p.smem = norm_smem(d->D, bwd);
         per_sm = std::min<long long>(per_sm, 220 * 1024 / (p.smem + 3 * 1024));
         if (bwd && per_sm == 1) p.threads = NORM_THREADS;
     }
@@ -557,7 +562,7 @@ NormPlan norm_plan(const sdm_norm_dims* d, bool bwd) {
 template <bool VEC>
 sdm_status launch_norm_wide(const NormArgs& a, bool bwd, const NormPlan& p, cudaStream_t s) {
     auto kernel = bwd ? block_norm_bwd_wide_kernel<VEC> : block_norm_wide_kernel<VEC>;
-    if (!allow_smem(kernel, p.smem)) return SDM_ERR_CUDA;
+    if (!allow_smem(kernel, p.smem, norm_smem(kNormMaxD, bwd))) return SDM_ERR_CUDA;
     kernel<<<p.blocks, p.threads, p.smem, s>>>(a);
     return launched();
 }

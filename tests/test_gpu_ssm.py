@@ -3,6 +3,8 @@ gradients, their forms for single tokens and padded batches, against the fp64 de
 tests/ssm_reference.py (which also derives the tolerances)."""
 from __future__ import annotations
 
+import threading
+
 import pytest
 import torch
 
@@ -483,6 +485,42 @@ def test_norm_rows_do_not_mix(sdm, D):
     assert want_o[600:].isfinite().all() and want_n[600:].isfinite().all()
     for k in ("dr", "df", "dgate"):
         assert normwise_rel_err(f64(want[k][600:]), ref[k].numpy()) < 1e-5, k
+
+
+@pytest.mark.parametrize("back", [False, True])
+def test_wide_norms_from_two_host_threads(sdm, back):
+    """Calls of different widths from two host threads: a kernel's shared memory is not allowed less
+    by one call than the other needs."""
+    status = {}
+
+    def calls(D):
+        torch.cuda.set_device(0)
+        s = torch.cuda.Stream()
+        d = sdm._NormDims(1, D, 0, 0, 0, 1e-6)
+        r, f, o, n, dr, df = (torch.ones(1, D, device="cuda") for _ in range(6))
+        ws = torch.empty(sdm._lib.sdm_block_norm_backward_workspace_bytes(d), dtype=torch.uint8, device="cuda")
+        torch.cuda.synchronize()
+        p = [t.data_ptr() for t in (r, f, o, n, dr, df, ws)]
+        bad = 0
+        for i in range(4000):
+            if back:
+                bad += sdm._lib.sdm_block_norm_backward(
+                    d, p[0], p[1], None, None, None, None, p[2], p[3], p[4], p[5], None, None, None, None,
+                    p[6], ws.numel(), s.cuda_stream) != 0
+            else:
+                bad += sdm._lib.sdm_block_norm(d, p[0], p[1], None, None, None, None, p[2], p[3],
+                                               s.cuda_stream) != 0
+            if i % 500 == 0:
+                s.synchronize()
+        s.synchronize()
+        status[D] = bad
+
+    threads = [threading.Thread(target=calls, args=(D,)) for D in (16384, 8192)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert status == {16384: 0, 8192: 0}
 
 
 # ---- as they are used ----------------------------------------------------------------------
