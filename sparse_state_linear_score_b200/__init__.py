@@ -865,7 +865,9 @@ def _norm_setup(r, f, x_dtype, eps):
     rdt, fdt = _act_dtype(r, "r"), _act_dtype(f, "f")
     if x_dtype not in _DT:
         raise TypeError(f"gate, n and dn are float32 or bfloat16, got {x_dtype}")
-    D = int(r.shape[-1]) if r.dim() else 0
+    if r.dim() == 0:
+        raise ValueError("r must be [..., D], got a tensor without dimensions")
+    D = int(r.shape[-1])
     return _norm_dims(r.numel() // D if D else 0, D, rdt, fdt, _DT[x_dtype], float(eps))
 
 

@@ -807,6 +807,15 @@ def test_binding_refuses(sdm):
             f()
 
 
+def test_norm_refuses_scalars(sdm):
+    """A tensor without dimensions has no last one: it is no row of one value, nor an empty call."""
+    s, m = torch.ones((), device="cuda"), torch.ones(2, 1, device="cuda")
+    for f in (lambda: sdm.block_norm(s, s), lambda: sdm.block_norm(s, m), lambda: sdm.block_norm(m, s),
+              lambda: sdm.block_norm_backward(s, s, s, None)):
+        with pytest.raises(ValueError):
+            f()
+
+
 def test_binding_refuses_sizes_beyond_its_fields(sdm):
     """2^32 + 4 tokens or columns are not taken for 4."""
     big, z = (1 << 32) + 4, torch.zeros(1, device="cuda")

@@ -191,3 +191,16 @@ def test_binding_sizes(dims, sizes):
         if isinstance(v, int) and not (dims == "_norm_dims" and i == 0):
             with pytest.raises(ValueError, match="too large"):
                 f(*sizes[:i], (1 << 32) + v, *sizes[i + 1:])
+
+
+def test_binding_refuses_norms_of_scalars(monkeypatch):
+    """A tensor without dimensions is not taken for an empty call, whose outputs nothing writes."""
+    import torch
+
+    import sparse_state_linear_score_b200 as m
+    monkeypatch.setattr(m, "_act_dtype", lambda t, what: 0)
+    s, r = torch.ones(()), torch.ones(2, 8)
+    with pytest.raises(ValueError, match="dimensions"):
+        m._norm_setup(s, s, torch.float32, 1e-6)
+    for t in (r, r[:0]):
+        assert m._norm_setup(t, t, torch.float32, 1e-6)[0].rows == len(t)
