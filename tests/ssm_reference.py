@@ -101,6 +101,37 @@ def conv_bwd(x, w, bias, act, state, lens, dy, dstate_end, mag=False):
     return {"dx": dx, "dw": dw, "dbias": db, "dstate": dst}
 
 
+def conv_all(x, w, bias, act, state, lens, dy, dstate_end):
+    """conv and conv_bwd for calls of many tokens, on x's device, all tokens at once -> (values,
+    magnitudes): dicts of y, state, dx, dw, dbias, dstate."""
+    B, H, T, d = x.shape
+    K = w.shape[2]
+    n = torch.tensor(_lens(lens, B, T), device=x.device)
+    m = (torch.arange(T, device=x.device) < n[:, None])[:, None, :, None]
+    x, dy = x.masked_fill(~m, 0), dy.masked_fill(~m, 0)
+    xp = torch.cat([state, x], dim=2)
+    at = (n[:, None, None, None] + torch.arange(K - 1, device=x.device)[:, None]).expand(B, H, K - 1, d)
+    tap = lambda v, j: v[:, :, j:j + T]  # noqa: E731
+    b = 0 if bias is None else bias[None, :, None]
+    p = sum(tap(xp, j) * w[None, :, None, :, j] for j in range(K)) + b
+    pa = sum(tap(xp, j).abs() * w[None, :, None, :, j].abs() for j in range(K)) + abs(b)
+    out = []
+    for mag in (False, True):
+        v = {"y": (1.1 * pa if mag else silu(p) if act else p) * m, "state": xp.gather(2, at)}
+        g = _ab(dy, mag)
+        if act:
+            g = g * (dsilu(p, True) + 0.5 * pa if mag else dsilu(p))
+        g = g * m
+        dxp = torch.zeros_like(xp).scatter_add_(2, at, _ab(dstate_end, mag))
+        for j in range(K):
+            tap(dxp, j).add_(g * _ab(w, mag)[None, :, None, :, j])
+        v["dx"], v["dstate"] = dxp[:, :, K - 1:] * m, dxp[:, :, :K - 1]
+        v["dw"] = torch.stack([(g * tap(_ab(xp, mag), j)).sum((0, 2)) for j in range(K)], dim=-1)
+        v["dbias"] = g.sum((0, 2))
+        out.append(v)
+    return out
+
+
 # ---- selective scan ------------------------------------------------------------------------
 
 def _rep(m, D):
@@ -229,6 +260,23 @@ def norm_bwd(r, f, dr_out, dn, w_post=None, gate=None, scale=None, w_pre=None, e
     return v, mag
 
 
+def along(rows, D, r, f, x, has, g, eps=1e-6, std=1.0):
+    """Inputs of a norm whose gradients lie along its rows, dn along o^ and dr_out along f^, so that
+    the means which the gradient takes off are of its own size (of independent ones they are
+    D^-1/2 of it, and a gradient without them would pass)."""
+    rnd = lambda dt, s=1.0: (torch.randn(rows, D, generator=g) * s).to(dt)  # noqa: E731
+    vec = [torch.rand(D, generator=g) + 0.5 for _ in range(3)]
+    rr, ff = rnd(r, std), rnd(f, std)
+    opt = {"w_post": vec[0] if has[0] else None, "gate": rnd(x) if has[1] else None,
+           "scale": vec[1] if has[2] else None, "w_pre": vec[2] if has[3] else None}
+    o, n = norm(rr.double(), ff.double(), **{k: None if v is None else v.double() for k, v in opt.items()},
+                eps=eps)
+    oh = n if opt["w_pre"] is None else n / opt["w_pre"].double()
+    dn = rnd(x).double() + oh / (1 if opt["w_pre"] is None else opt["w_pre"].double())
+    dr = rnd(r).double() + ff.double() / std
+    return rr, ff, opt, dr.to(r), dn.to(x)
+
+
 # ---- checks --------------------------------------------------------------------------------
 
 def within(got, ref, mag, roundings, what):
@@ -242,3 +290,10 @@ def within(got, ref, mag, roundings, what):
     bad = ~(err <= tol)
     assert not bad.any(), (f"{what}: {int(bad.sum())} of {bad.numel()} off, worst "
                            f"{float((err / tol).nan_to_num(float('inf')).max()):.3g} of its bound")
+
+
+def off(got, ref):
+    """|got - ref| / |ref|, of the whole tensors."""
+    got, ref = got.detach().double(), ref.to(got.device)
+    assert got.shape == ref.shape, (got.shape, ref.shape)
+    return float((got - ref).norm() / ref.norm())

@@ -77,3 +77,39 @@ def test_norm_formulas(full):
     for k, a in zip(names, grads):
         _close(got[k], a, k)
         assert (mag[k] >= got[k].abs() * (1 - 1e-12)).all(), k
+
+
+@pytest.mark.parametrize("K,act,lens,bias", [(1, True, None, True), (4, False, [5, 2, 0], True),
+                                             (8, True, [6, 1, 6], False)])
+def test_conv_of_all_tokens_at_once(K, act, lens, bias):
+    g = torch.Generator().manual_seed(K)
+    r = lambda *n: torch.randn(n, generator=g, dtype=torch.float64)  # noqa: E731
+    B, H, T, d = 3, 2, 6, 3
+    x, w, b, st = r(B, H, T, d), r(H, d, K), r(H, d) if bias else None, r(B, H, K - 1, d)
+    dy, de = r(B, H, T, d), r(B, H, K - 1, d)
+    for mag, got in zip((False, True), R.conv_all(x, w, b, act, st, lens, dy, de)):
+        y, end = R.conv(x, w, b, act, st, lens, mag)
+        want = dict(R.conv_bwd(x, w, b, act, st, lens, dy, de, mag), y=y)
+        if not mag:
+            want["state"] = end
+        for k in want:
+            _close(got[k], want[k], (k, mag))
+
+
+@pytest.mark.parametrize("rows,D,dt", [(3, 16384, torch.bfloat16), (2, 16383, torch.float32),
+                                       (2, 8191, torch.float32), (5, 64, torch.float32)])
+def test_norm_gradients_without_a_mean_are_told_apart(rows, D, dt):
+    """The check that the kernels' gradients pass on R.along's inputs rejects a gradient that leaves
+    out mean(m o^) in dr, or mean(q f^) in df."""
+    rr, ff, opt, dro, dn = R.along(rows, D, dt, dt, dt, (1, 1, 1, 1), torch.Generator().manual_seed(D))
+    r, f, dr0, m0 = (v.double() for v in (rr, ff, dro, dn))
+    o64 = {k: v.double() for k, v in opt.items()}
+    ref, _ = R.norm_bwd(r, f, dr0, m0, **o64)
+    o, _ = R.norm(r, f, **o64)
+    ro = 1 / torch.sqrt((o * o).mean(-1, keepdim=True) + 1e-6)
+    rf = 1 / torch.sqrt((f * f).mean(-1, keepdim=True) + 1e-6)
+    share = o64["scale"] * R.sigmoid(o64["gate"]) * o64["w_post"]
+    for name, do in (("dr", dr0 + ro * m0 * o64["w_pre"]), ("df", ref["dr"])):
+        bad = do if name == "dr" else rf * do * share
+        assert R.off(ref[name].to(dt), ref[name]) <= 2.0 ** -8
+        assert R.off(bad.to(dt), ref[name]) > 0.05, name
