@@ -602,8 +602,9 @@ __global__ void __launch_bounds__(32, 8) scan_walk_kernel(ScanArgs<T> a) {
 
 // Chains the chunks: E[k] becomes the state that chunk k starts from and, in the gradient (the
 // grid's second row), R[k] the carry that reaches its last token.  One thread a state; the loads of
-// SCAN_AHEAD chunks are in flight together.  Bound by memory: both directions of 2 x 64 chunks of
-// 2048 x 16 states, 67 MB read and 67 MB written, take 20 us.
+// SCAN_AHEAD chunks are in flight together.  Both directions of 2 x 64 chunks of 2048 x 16 states,
+// 34 MB read and 34 MB written, take 20 us: 3.4 TB/s, half of the copy rate, bound by the latency of a
+// thread's chunks in turn.
 constexpr int SCAN_AHEAD = 8;
 template <typename T>
 __global__ void __launch_bounds__(256) scan_carry_kernel(ScanArgs<T> a) {

@@ -24,8 +24,10 @@
 //
 // Bound by issue and shared memory: about 155 instructions and 37 shared-memory cycles a token and
 // eight channels of 16 states.  2 sequences of 2048 tokens, 2048 channels, bf16: 266 us (issue 58 %,
-// shared memory 53 %), with the walks, carries and sums 361 us; three passes over the exponentials
-// alone are 90 us.
+// shared memory 53 %), with the walks, carries and sums 363 us; three passes over the exponentials
+// alone are 90 us.  Three blocks live on an SM in bf16 with 9 to 32 states, in the other forms two (of
+// fp32 with up to 8 states one), by their shared memory; all are compiled for three, 168 registers,
+// and spill 20 to 128 bytes a thread.
 #pragma once
 
 #include "selective_scan.cuh"

@@ -409,8 +409,8 @@ ScanBwdPlan scan_bwd_plan(const sdm_scan_dims* d) {
     p.nchunk = (int)std::max(1LL, ceil_div(d->T, BWD_CHUNK));
     // A block's channels go by turns of its warps: more turns, fewer shares of dB and dC to write and
     // add; fewer turns, more blocks to even the SMs' work out.  Fourteen blocks an SM, of which
-    // three run at a time, did best (2 sequences of 2048 tokens, 2048 channels: 361 us in 2048
-    // blocks, 368 us in 896, 390 us in 384, 407 us in 8192).
+    // three run at a time, did best (bf16, 16 states, the only form compared: 2 sequences of 2048
+    // tokens, 2048 channels: 361 us in 2048 blocks, 368 us in 896, 390 us in 384, 407 us in 8192).
     const int ch = BWD_WARPS * 32 / (p.NN / 4), all = (int)ceil_div(d->D / d->G, ch);
     const long long rest = (long long)d->B * p.nchunk * d->G;
     const long long want = std::max(1LL, std::min<long long>(all, 14 * kSms / rest));
