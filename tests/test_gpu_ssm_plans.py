@@ -235,3 +235,109 @@ def test_backward_of_fresh_calls(sdm, T, dtype):
                                                      dstate_end=up(de))
     got, want = f(up(st).fill_(float("nan")), True), f(up(st).zero_(), False)
     assert got.keys() == want.keys() and all(torch.equal(got[k], want[k]) for k in want)
+
+
+# ---- the ends of the ranges ------------------------------------------------------------------
+
+@pytest.mark.parametrize("B,H,T,d,dtype,cut", [
+    (65535, 1, 1100, 4, "bf16", 7),        # runs as long as the grid's second axis asks for
+    (2, 3, 45, 100001, "bf16", 1),         # more columns of blocks than the gradient wants blocks
+    (3, 1, 70, 80000, "f32", 2),
+    (1, 1, 5_000_001, 4, "bf16", None),
+])
+def test_conv_of_many_sequences_channels_or_tokens(sdm, B, H, T, d, dtype, cut):
+    """The batch's parts give bit for bit what the whole gives, and the filters' gradients add up."""
+    g = torch.Generator("cuda").manual_seed(1)
+    r = lambda *n, dt=torch.float32: torch.randn(n, generator=g, device="cuda").to(dt)  # noqa: E731
+    x, dy = r(B, H, T, d, dt=DT[dtype]), r(B, H, T, d, dt=DT[dtype])
+    w, st = r(H, d, 4), r(B, H, 3, d, dt=DT[dtype])
+    s1, s2 = st.clone(), st.clone()
+    y, got = sdm.short_conv(x, w, state=s1), sdm.short_conv_backward(x, w, dy, state=st)
+    if cut is None:  # tokens instead of sequences
+        t = T // 3
+        parts = [sdm.short_conv(v, w, state=s2) for v in (x[:, :, :t], x[:, :, t:])]
+        assert torch.equal(torch.cat(parts, 2), y) and torch.equal(s1, s2)
+        for a in (0, T - 2000):  # dx of the last tokens of a part needs the tokens behind it
+            before = st if a == 0 else x[:, :, a - 3:a]
+            p, q = (v[:, :, a:a + 2000].double() for v in (x, dy))
+            ref, mag = R.conv_all(p, w.double(), None, True, before.double(), None, q, torch.zeros_like(st).double())
+            n = 2000 if a else 1997
+            near(got["dx"][:, :, a:a + n], ref["dx"][:, :, :n], mag["dx"][:, :, :n], 2 * 4 + 2 + 128, "dx")
+        return
+    s2 = [s2[:cut].clone(), s2[cut:].clone()]  # starts at 16 bytes
+    cuts = ((0, cut), (cut, B))
+    parts = [sdm.short_conv(x[a:b], w, state=v) for (a, b), v in zip(cuts, s2)]
+    assert torch.equal(torch.cat(parts), y) and torch.equal(s1, torch.cat(s2))
+    p = [sdm.short_conv_backward(x[a:b], w, dy[a:b], state=st[a:b].clone()) for a, b in cuts]
+    for k in ("dx", "dstate"):
+        assert torch.equal(torch.cat([v[k] for v in p]), got[k])
+    close(got["dw"], p[0]["dw"].double() + p[1]["dw"].double(), "dw", 5e-5)
+
+
+@pytest.mark.parametrize("B,T,D,N,G,dtype", [
+    (65535, 3, 4, 8, 1, "bf16"), (65535, 1, 4, 8, 1, "f32"), (2, 90, 300, 16, 300, "bf16"),
+    (3, 40, 21000, 1, 21000, "f32"), (3, 100, 70001, 3, 1, "bf16"),
+])
+def test_scan_of_many_sequences_groups_or_channels(sdm, B, T, D, N, G, dtype):
+    g = torch.Generator("cuda").manual_seed(2)
+    r = lambda *n, dt=DT[dtype]: torch.randn(n, generator=g, device="cuda").to(dt)  # noqa: E731
+    u, de, z, dy, Bm, Cm = r(B, T, D), r(B, T, D), r(B, T, D), r(B, T, D), r(B, T, G, N), r(B, T, G, N)
+    A, st = -torch.rand(D, N, generator=g, device="cuda") - 0.05, r(B, D, N, dt=torch.float32)
+    s1, s2 = st.clone(), st.clone()
+    y = sdm.selective_scan(u, de, A, Bm, Cm, z=z, state=s1)
+    got = sdm.selective_scan_backward(u, de, A, Bm, Cm, dy, z=z, state=st)
+    c = B // 2
+    cuts = ((0, c), (c, B))
+    s2 = [s2[:c].clone(), s2[c:].clone()]  # starts at 16 bytes
+    parts = [sdm.selective_scan(u[a:b], de[a:b], A, Bm[a:b], Cm[a:b], z=z[a:b], state=v)
+             for (a, b), v in zip(cuts, s2)]
+    back = [sdm.selective_scan_backward(u[a:b], de[a:b], A, Bm[a:b], Cm[a:b], dy[a:b], z=z[a:b],
+                                        state=st[a:b].clone()) for a, b in cuts]
+    close(torch.cat(parts), y.double(), "y")
+    close(torch.cat(s2), s1.double(), "state")
+    for k in ("du", "ddelta", "dz", "dB", "dC", "dstate"):
+        close(torch.cat([v[k] for v in back]), got[k].double(), k, 5e-5)
+    close(got["dA"], back[0]["dA"].double() + back[1]["dA"].double(), "dA", 5e-5)
+
+
+def test_scan_of_the_most_tokens(sdm):
+    """2,097,120 tokens, 65,535 chunks of the gradient, against calls of a part of them."""
+    B, T, D, N = 1, 2_097_120, 2, 2
+    g = torch.Generator("cuda").manual_seed(3)
+    r = lambda *n: torch.randn(n, generator=g, device="cuda")  # noqa: E731
+    u, de, dy, Bm, Cm = r(B, T, D), r(B, T, D), r(B, T, D), r(B, T, 1, N), r(B, T, 1, N)
+    A = -torch.rand(D, N, generator=g, device="cuda") - 0.05
+    s1, s2 = torch.zeros(B, D, N, device="cuda"), torch.zeros(B, D, N, device="cuda")
+    y = sdm.selective_scan(u, de, A, Bm, Cm, state=s1)
+    got = sdm.selective_scan_backward(u, de, A, Bm, Cm, dy)
+    c = T // 3 + 5
+    cut = lambda v: (v[:, :c], v[:, c:])  # noqa: E731
+    parts, mid = [], None
+    for q in range(2):
+        if q:
+            mid = s2.clone()
+        parts.append(sdm.selective_scan(cut(u)[q], cut(de)[q], A, cut(Bm)[q], cut(Cm)[q], state=s2))
+    close(torch.cat(parts, 1), y.double(), "y")
+    close(s2, s1.double(), "state")
+    late = sdm.selective_scan_backward(cut(u)[1], cut(de)[1], A, cut(Bm)[1], cut(Cm)[1], cut(dy)[1], state=mid)
+    early = sdm.selective_scan_backward(cut(u)[0], cut(de)[0], A, cut(Bm)[0], cut(Cm)[0], cut(dy)[0],
+                                        state=torch.zeros_like(mid), dstate_end=late["dstate"])
+    for k in ("du", "ddelta", "dB", "dC"):
+        close(torch.cat([early[k], late[k]], 1), got[k].double(), k, 5e-5)
+    close(got["dA"], early["dA"].double() + late["dA"].double(), "dA", 5e-5)
+
+
+def test_norm_of_more_than_2_31_values(sdm):
+    rows, D = 530_000, 4096  # 2.17e9 values
+    r, f = (torch.empty(rows, D, dtype=torch.bfloat16, device="cuda").normal_() for _ in range(2))
+    w = torch.rand(D, device="cuda") + 0.5
+    o, n = sdm.block_norm(r, f, w_post=w, w_pre=w)
+    g = sdm.block_norm_backward(r, f, r, f, w_post=w, w_pre=w)
+    for a, b in ((0, 300), (rows - 300, rows), (rows // 2, rows // 2 + 300)):
+        o2, n2 = sdm.block_norm(r[a:b].contiguous(), f[a:b].contiguous(), w_post=w, w_pre=w)
+        g2 = sdm.block_norm_backward(r[a:b].contiguous(), f[a:b].contiguous(), r[a:b].contiguous(),
+                                     f[a:b].contiguous(), w_post=w, w_pre=w)
+        assert torch.equal(o[a:b], o2) and torch.equal(n[a:b], n2)
+        for k in ("dr", "df"):  # a block's first row sums f^2 in another order: a step of bf16 at most
+            d = (g[k][a:b].float() - g2[k].float()).abs()
+            assert (d <= 2.0 ** -7 * g2[k].float().abs() + 1e-5).all(), k
