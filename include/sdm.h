@@ -478,7 +478,8 @@ sdm_status sdm_weight_stats(int64_t rows, int32_t K, const float* w, float* cum,
  *
  * Padded batches: lens [B] int32 (device, or NULL: every sequence has T tokens; 4-byte aligned)
  * are the tokens of each sequence, taken as clamped to [0, T].  Tokens behind them are not read,
- * move no state and leave their output rows as they were; their gradients are written as zero.
+ * move no state and leave their output rows as they were; their gradients are written as zero.  A
+ * sequence of no tokens adds nothing to a sum over the batch, whatever its state holds.
  *
  * Sums, states and the norms' means are fp32; each output is rounded once to its type.
  * Every result is the same from run to run (no atomics: sums over blocks are added in order).
